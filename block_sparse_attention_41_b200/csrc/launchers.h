@@ -110,6 +110,82 @@ cudaError_t launch_quant_v8(const QuantV8Args& a, cudaStream_t stream);
 // bf16, d in {64, 128}: QK RMS norm + rotary embedding + K/V block pooling in one pass.
 cudaError_t launch_qknorm_rope_pool(const RopePoolArgs& a, cudaStream_t stream);
 
+// Gated residual and norm (sol_attn_residual_norm); null vectors are absent.
+enum : int { NORM_NONE = 0, NORM_LAYER = 1, NORM_RMS = 2 };
+constexpr int kNormMaxC = 8192;
+struct NormArgs {
+  const void* x;  // [B, T, C]
+  const void* y;  // [B, T, C] or null: no residual step, x is normalised as it is
+  const float* gate;  // rows of C, one per batch entry, gate_stride floats apart
+  long long gate_stride;
+  const float* gain;  // [C]
+  const float* scale;
+  long long scale_stride;
+  const float* shift;
+  long long shift_stride;
+  const float* post_gain;  // [C]
+  void* x_out;  // with y: [B, T, C]
+  void* h;      // [B, T, C]
+  int B, T, C;
+  int norm, post_norm;
+  float res_scale, eps;
+  bool bf16;
+  bool vec;  // rows and vectors allow 16-byte accesses
+};
+cudaError_t launch_residual_norm(const NormArgs& a, cudaStream_t stream);
+
+// Its gradients. fwd.x_out, fwd.h and fwd.shift are not read.
+struct NormBwdArgs {
+  NormArgs fwd;
+  const void* dh;      // [B, T, C]
+  const void* dx_out;  // [B, T, C] or null
+  void* dx;            // [B, T, C]
+  void* dy;            // with y: [B, T, C]
+  float* dgate;        // [B, C] or null, as the next two
+  float* dscale;
+  float* dshift;
+  float* dgain;        // [C] or null
+  float* dpost_gain;   // [C] or null
+  float* part;         // workspace of norm_bwd_part_floats, or null where no vector's gradient is wanted
+  int C, chunks;       // chunks = norm_bwd_chunks(B, T, C)
+};
+constexpr int kNormBwdBlocks = 592;  // blocks over all batch entries: 4 per SM
+int norm_bwd_chunks(int B, int T, int C);
+size_t norm_bwd_part_floats(int B, int T, int C);
+cudaError_t launch_residual_norm_bwd(const NormBwdArgs& a, cudaStream_t stream);
+
+// Rotary positions (sol_attn_rope): rows of Q and K, each [B, heads, L, d] with its own strides.
+struct RopeSide {
+  const void* in;
+  void* out;
+  int heads;
+  long long in_b, in_h, in_l;     // strides in elements; the d channels are contiguous
+  long long out_b, out_h, out_l;
+};
+struct RopeArgs {
+  RopeSide side[2];
+  const int* pos;        // [axes, L], pos_b apart per batch entry
+  long long pos_b;
+  const double* inv_freq;  // [rot / 2]
+  int B, L, d, rot, axes;
+  int end[4];            // pairs [end[a - 1], end[a]) turn by axis a
+  float factor;
+  bool half, inverse, bf16;
+  bool vec;              // 16-byte accesses
+  bool copy_rest;        // channels [rot, d) have to be written too
+};
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);
+struct RopeTableArgs {
+  const int* pos;  // [axes, L]
+  const double* inv_freq;
+  int L, rot, axes;
+  int end[4];
+  float factor;
+  float* cos;  // [L, rot / 2]
+  float* sin;
+};
+cudaError_t launch_rope_tables(const RopeTableArgs& a, cudaStream_t stream);
+
 // bf16, d in {64, 128}, block 128: routing pass for every unit (q_bar kernel, then the routing
 // kernel); writes a.route_qbar, a.route_bits, the optional mask and the per-head kept counts
 // (ws + WS_COUNTS).

@@ -8,6 +8,7 @@
 #include <mutex>
 #include <string>
 
+#include "api_common.h"
 #include "device_common.cuh"
 #include "launchers.h"
 #include "sol_attn.h"
@@ -18,6 +19,13 @@ thread_local std::string g_last_error;
 int g_drop_one_load = 0;  // failure-detection test hook, consumed by the next bf16 launch
 unsigned long long* g_cta_times = nullptr;  // measurement hook, consumed by the next bf16 launch
 int g_cta_capacity = 0;
+
+}  // namespace
+
+namespace sol {
+namespace api {
+
+void clear_error() { g_last_error.clear(); }
 
 sol_status fail(sol_status s, const char* fmt, ...) {
   char buf[512];
@@ -32,8 +40,6 @@ sol_status fail(sol_status s, const char* fmt, ...) {
 sol_status cuda_fail(cudaError_t e, const char* what) {
   return fail(SOL_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Device checks: an sm_100 GPU is current. Returns SOL_OK and its SM count.
 sol_status current_device(int* num_sms) {
@@ -53,10 +59,6 @@ sol_status current_device(int* num_sms) {
 }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link-time libcuda).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
   static std::once_flag once;
   static EncodeTiledFn fn = nullptr;
@@ -69,6 +71,13 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
+
+}  // namespace api
+}  // namespace sol
+
+namespace {
+
+using namespace sol::api;
 
 // 3-D view [BH][rows][d] with 128-byte-wide x 128 x 1 boxes (64 bf16 or 128 int8 values) and
 // 128-byte swizzle. Rows past `rows` (a ragged last block) are zero-filled by the copy engine.
@@ -87,8 +96,6 @@ sol_status make_map(CUtensorMap* m, const void* base, int d, int rows, int BH, b
   if (r != CUDA_SUCCESS) return fail(SOL_ECUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
   return SOL_OK;
 }
-
-bool size_ok(long long v, long long lim) { return v >= 1 && v <= lim; }
 
 // Workspace layout: [error, where, counter, done, counts[B*H]] rounded to 256 B (the header), then
 // the keep bits of the routing pass, u32[B*H][N_qb][ceil(N_kb/32)].

@@ -41,7 +41,18 @@ EXPORTED = (
     "sol_attn_fwd_qbar",
     "sol_attn_quantize_v8",
     "sol_attn_fwd_8bit",
+    "sol_attn_residual_norm",
+    "sol_attn_residual_norm_bwd",
+    "sol_attn_residual_norm_bwd_workspace_bytes",
+    "sol_attn_rope_inv_freq",
+    "sol_attn_rope_tables",
+    "sol_attn_rope",
 )
+
+# names of the enumerations of the dense operators
+NORMS = {"none": 0, "layer": 1, "rms": 2}
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class SolAttnError(RuntimeError):
@@ -107,6 +118,24 @@ def load_library() -> ctypes.CDLL:
     lib.sol_attn_fwd_topk.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp,
                                       ctypes.c_size_t, vp]
     lib.sol_attn_fwd_topk.restype = i32
+    i64, f32, f64, i64p, i32p = ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.POINTER(ctypes.c_int64), \
+        ctypes.POINTER(ctypes.c_int)
+    size = ctypes.c_size_t
+    lib.sol_attn_residual_norm.argtypes = [vp, vp, vp, i64, vp, vp, i64, vp, i64, vp, i32, i32, i32, f32, f32, i32, i32,
+                                           i32, vp, vp, vp]
+    lib.sol_attn_residual_norm.restype = i32
+    lib.sol_attn_residual_norm_bwd_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.sol_attn_residual_norm_bwd_workspace_bytes.restype = size
+    lib.sol_attn_residual_norm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, i64, vp, i32, i32, i32, f32, f32, i32,
+                                               i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
+    lib.sol_attn_residual_norm_bwd.restype = i32
+    lib.sol_attn_rope_inv_freq.argtypes = [i32, f64, i32, i32p, i32, f64, f64, f64, f64, ctypes.POINTER(f64), f32p]
+    lib.sol_attn_rope_inv_freq.restype = i32
+    lib.sol_attn_rope_tables.argtypes = [vp, i32, i32p, vp, f32, i32, i32, vp, vp, vp]
+    lib.sol_attn_rope_tables.restype = i32
+    lib.sol_attn_rope.argtypes = [vp, i64p, vp, i64p, i32, vp, i64, i32, i32p, vp, f32, i32, i32, i32, i32, i32, i32, i32,
+                                  i32, vp, i64p, vp, i64p, vp]
+    lib.sol_attn_rope.restype = i32
     lib.sol_attn_check_device_error.argtypes = [vp, vp]
     lib.sol_attn_check_device_error.restype = i32
     lib.sol_attn_debug_drop_one_load.argtypes = [i32]
@@ -519,3 +548,252 @@ def sol_attn_fwd_host(Q, K, V, tau, block: int = 128, n_force: int = 0, heads_pe
 def tau_list(values) -> list:
     """Turn a JSON-style tau list ("inf" strings allowed) into floats."""
     return [math.inf if (isinstance(v, str) and v.lower() == "inf") else float(v) for v in values]
+
+
+# ---- dense operators around the attention ----------------------------------------------------------
+
+class _On:
+    """The tensors' device made current, and the caller's stream (default: the device's current one)
+    made torch's, so that what a call allocates belongs to the stream that its kernels run on."""
+
+    __slots__ = ("device", "stream", "_contexts")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self._contexts = device, stream, ()
+
+    def __enter__(self):
+        if self.stream is not None:
+            s = self.stream
+            if not hasattr(s, "cuda_stream"):
+                s = torch.cuda.ExternalStream(int(s), device=self.device)
+            elif s.device != self.device:
+                raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
+            self._contexts = (torch.cuda.stream(s),)
+        elif torch.cuda.current_device() != self.device.index:
+            self._contexts = (torch.cuda.device(self.device),)
+        for c in self._contexts:
+            c.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in self._contexts:
+            c.__exit__(*exc)
+        return False
+
+
+def _need_cuda_on(name: str, t, device, dtype=None) -> None:
+    """_need_cuda without the contiguity, on the given device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+
+
+def _need_like(name: str, t, ref) -> None:
+    """A contiguous CUDA tensor of ref's device, dtype and shape."""
+    _need_cuda_on(name, t, ref.device, ref.dtype)
+    if t.shape != ref.shape:
+        raise ValueError(f"{name} must have shape {tuple(ref.shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _need_vector(name: str, t, device, C: int) -> None:
+    if t is None:
+        return
+    _need_cuda_on(name, t, device, torch.float32)
+    if tuple(t.shape) != (C,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {C} values")
+
+
+def _need_rows(name: str, t, device, B: int, C: int) -> int:
+    """Checks [B, C] fp32 rows (channels contiguous) and returns their stride."""
+    if t is None:
+        return 0
+    _need_cuda_on(name, t, device, torch.float32)
+    if tuple(t.shape) != (B, C) or (C > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [B, C] = [{B}, {C}] with contiguous channels")
+    return t.stride(0) if B > 1 else 0
+
+
+def _choice(name: str, value, names: dict) -> int:
+    try:
+        return names[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {sorted(names)}, got {value!r}") from None
+
+
+def _check_norm(x, y, gate, gain, scale, shift, post_gain):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    if x.dim() != 3 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [B, T, C] tensor")
+    B, T, C = x.shape
+    if y is not None:
+        _need_like("y", y, x)
+    _need_vector("gain", gain, x.device, C)
+    _need_vector("post_gain", post_gain, x.device, C)
+    return (B, T, C) + tuple(_need_rows(n, t, x.device, B, C) for n, t in (("gate", gate), ("scale", scale),
+                                                                          ("shift", shift)))
+
+
+def sol_attn_residual_norm(x, y=None, gate=None, gain=None, scale=None, shift=None, post_gain=None, norm="layer",
+                           post_norm="none", res_scale: float = 1.0, eps: float = 1e-6, x_out=None, h=None, stream=None):
+    """x' = res_scale x + gate * post_norm(y) post_gain and h = norm(x') gain (1 + scale) + shift, in one
+    pass. x, y: [B, T, C]; gate, scale, shift: fp32 [B, C] (row stride free); gain, post_gain: fp32
+    [C]; norms "layer" or "rms", post_norm also "none". Returns (x', h); without y, (x, h)."""
+    B, T, C, gs, ss, hs = _check_norm(x, y, gate, gain, scale, shift, post_gain)
+    dt, n, pn = _dtype_code(x), _choice("norm", norm, NORMS), _choice("post_norm", post_norm, NORMS)
+    if x_out is not None:
+        _need_like("x_out", x_out, x)
+    if h is not None:
+        _need_like("h", h, x)
+    with _On(x.device, stream) as s:
+        if y is not None and x_out is None:
+            x_out = torch.empty_like(x)
+        if h is None:
+            h = torch.empty_like(x)
+        st = load_library().sol_attn_residual_norm(
+            _ptr(x), _ptr(y), _ptr(gate), gs, _ptr(gain), _ptr(scale), ss, _ptr(shift), hs, _ptr(post_gain), dt, n, pn,
+            res_scale, eps, B, T, C, _ptr(x_out), _ptr(h), s)
+    _check(st, "sol_attn_residual_norm")
+    return (x if y is None else x_out), h
+
+
+def sol_attn_residual_norm_bwd(dh, x, y=None, gate=None, gain=None, scale=None, post_gain=None, dx_out=None,
+                               norm="layer", post_norm="none", res_scale: float = 1.0, eps: float = 1e-6,
+                               want_dshift: Optional[bool] = None, workspace=None, stream=None) -> dict:
+    """Gradients of sol_attn_residual_norm from its inputs, dh (gradient of h) and dx_out (what reaches
+    x' from elsewhere). Returns a dict of dx, dy and, for each vector given, dgate, dgain, dscale,
+    dpost_gain (fp32, the vector's shape), and dshift where want_dshift (default: with scale); None
+    for the others."""
+    B, T, C, gs, ss, _ = _check_norm(x, y, gate, gain, scale, None, post_gain)
+    dt, n, pn = _dtype_code(x), _choice("norm", norm, NORMS), _choice("post_norm", post_norm, NORMS)
+    _need_like("dh", dh, x)
+    if dx_out is not None:
+        _need_like("dx_out", dx_out, x)
+    if workspace is not None:
+        _need_cuda_on("workspace", workspace, x.device, torch.uint8)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    want_dshift = scale is not None if want_dshift is None else want_dshift
+    lib = load_library()
+    with _On(x.device, stream) as s:
+        def new(want, *shape):
+            return torch.empty(shape, dtype=torch.float32, device=x.device) if want else None
+        g = {"dx": torch.empty_like(x), "dy": None if y is None else torch.empty_like(x),
+             "dgate": new(gate is not None, B, C), "dgain": new(gain is not None, C),
+             "dscale": new(scale is not None, B, C), "dshift": new(want_dshift, B, C),
+             "dpost_gain": new(post_gain is not None, C)}
+        if workspace is None and any(g[k] is not None for k in ("dgate", "dgain", "dscale", "dshift", "dpost_gain")):
+            workspace = torch.empty(lib.sol_attn_residual_norm_bwd_workspace_bytes(B, T, C), dtype=torch.uint8,
+                                    device=x.device)
+        st = lib.sol_attn_residual_norm_bwd(
+            _ptr(dh), _ptr(dx_out), _ptr(x), _ptr(y), _ptr(gate), gs, _ptr(gain), _ptr(scale), ss, _ptr(post_gain), dt, n,
+            pn, res_scale, eps, B, T, C, _ptr(g["dx"]), _ptr(g["dy"]), _ptr(g["dgate"]), _ptr(g["dgain"]),
+            _ptr(g["dscale"]), _ptr(g["dshift"]), _ptr(g["dpost_gain"]), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), s)
+    _check(st, "sol_attn_residual_norm_bwd")
+    return g
+
+
+def _int_array(values):
+    return None if values is None else (ctypes.c_int * len(values))(*[int(v) for v in values])
+
+
+def sol_attn_rope_inv_freq(rot: int, base: float = 10000.0, sections=None, scaling: str = "none", factor: float = 1.0,
+                           original_length: float = 8192.0, turns_low: float = 1.0, turns_high: float = 32.0,
+                           device=None):
+    """Angular step of each rotary pair (float64 [rot / 2], on `device`, default CPU) and the factor on
+    cosine and sine. sections: pairs per position axis (default: one axis)."""
+    n = len(sections) if sections is not None else 1
+    f = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    m = ctypes.c_float(1.0)
+    st = load_library().sol_attn_rope_inv_freq(
+        int(rot), base, n, _int_array(sections), _choice("scaling", scaling, ROPE_SCALINGS), factor, original_length,
+        turns_low, turns_high, ctypes.cast(ctypes.c_void_p(f.data_ptr()), ctypes.POINTER(ctypes.c_double)),
+        ctypes.byref(m))
+    _check(st, "sol_attn_rope_inv_freq")
+    return (f if device is None else f.to(device)), float(m.value)
+
+
+def _check_positions(pos, inv_freq, sections, device, L: int, B: Optional[int]):
+    """(axes, sections array, stride of a batch entry's positions)."""
+    _need_cuda_on("pos", pos, device, torch.int32)
+    _need_cuda_on("inv_freq", inv_freq, device, torch.float64)
+    if not pos.is_contiguous() or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+        raise ValueError("pos and inv_freq must be contiguous, inv_freq a vector")
+    axes = len(sections) if sections is not None else 1
+    shapes = [(axes, L)] + ([(L,)] if axes == 1 else []) + ([(B, axes, L)] if B is not None else [])
+    if tuple(pos.shape) not in shapes:
+        raise ValueError(f"pos must have one of the shapes {shapes}, got {tuple(pos.shape)}")
+    return axes, _int_array(sections), (axes * L if pos.dim() == 3 else 0)
+
+
+def sol_attn_rope_tables(pos, inv_freq, sections=None, attn_factor: float = 1.0, rope_cos=None, rope_sin=None,
+                         stream=None):
+    """Cosine and sine tables (fp32 [L, rot / 2]) for sol_attn_qknorm_rope_pool: pos int32 [L] or
+    [axes, L], inv_freq float64 [rot / 2]. Returns (rope_cos, rope_sin)."""
+    if not isinstance(pos, torch.Tensor) or not pos.is_cuda:
+        raise TypeError("pos must be a CUDA tensor")
+    dev, L = pos.device, pos.shape[-1] if pos.dim() else 0
+    axes, sec, _ = _check_positions(pos, inv_freq, sections, dev, L, None)
+    half = inv_freq.numel()
+    for n, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
+        if t is not None:
+            _need_cuda_on(n, t, dev, torch.float32)
+            if tuple(t.shape) != (L, half) or not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous [{L}, {half}] tensor")
+    with _On(dev, stream) as s:
+        rope_cos = torch.empty((L, half), dtype=torch.float32, device=dev) if rope_cos is None else rope_cos
+        rope_sin = torch.empty((L, half), dtype=torch.float32, device=dev) if rope_sin is None else rope_sin
+        st = load_library().sol_attn_rope_tables(_ptr(pos), axes, sec, _ptr(inv_freq), attn_factor, L, 2 * half,
+                                                 _ptr(rope_cos), _ptr(rope_sin), s)
+    _check(st, "sol_attn_rope_tables")
+    return rope_cos, rope_sin
+
+
+def sol_attn_rope(Q, K, pos, inv_freq, layout: str = "interleaved", sections=None, attn_factor: float = 1.0,
+                  inverse: bool = False, Q_out=None, K_out=None, stream=None):
+    """Rotary positions of Q [B, Hq, L, d] and K [B, Hk, L, d] (or None), any strides with contiguous
+    channels; pos int32 [L], [axes, L] or [B, axes, L]; inv_freq float64 [rot / 2] from
+    sol_attn_rope_inv_freq. inverse=True turns back: the gradient. Outputs default to contiguous
+    tensors; pass Q_out=Q, K_out=K to work in place. Returns (Q_out, K_out)."""
+    if not isinstance(Q, torch.Tensor) or not Q.is_cuda:
+        raise TypeError("Q must be a CUDA tensor")
+    if Q.dim() != 4:
+        raise ValueError("Q must be [B, Hq, L, d]")
+    B, Hq, L, d = Q.shape
+    dt, lay = _dtype_code(Q), _choice("layout", layout, ROPE_LAYOUTS)
+    if K is None:
+        if K_out is not None:
+            raise ValueError("K_out needs K")
+    else:
+        _need_cuda_on("K", K, Q.device, Q.dtype)
+        if K.dim() != 4 or K.shape[0] != B or tuple(K.shape[2:]) != (L, d):
+            raise ValueError("K must be [B, Hk, L, d] with the B, L and d of Q")
+    for n, t, ref in (("Q_out", Q_out, Q), ("K_out", K_out, K)):
+        if t is not None:
+            _need_cuda_on(n, t, Q.device, Q.dtype)
+            if t.shape != ref.shape:
+                raise ValueError(f"{n} must have shape {tuple(ref.shape)}")
+    for n, t in (("Q", Q), ("K", K), ("Q_out", Q_out), ("K_out", K_out)):
+        if t is not None and d > 1 and t.stride(3) != 1:
+            raise ValueError(f"{n}'s channels must be contiguous")
+    axes, sec, pos_b = _check_positions(pos, inv_freq, sections, Q.device, L, B)
+
+    def strides(t):
+        return None if t is None else (ctypes.c_int64 * 3)(*t.stride()[:3])
+    with _On(Q.device, stream) as s:
+        if Q_out is None:
+            Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        if K is not None and K_out is None:
+            K_out = torch.empty(K.shape, dtype=K.dtype, device=K.device)
+        st = load_library().sol_attn_rope(
+            _ptr(Q), strides(Q), _ptr(K), strides(K), dt, _ptr(pos), pos_b, axes, sec, _ptr(inv_freq), attn_factor, lay,
+            int(bool(inverse)), B, Hq, 0 if K is None else K.shape[1], L, d, 2 * inv_freq.numel(), _ptr(Q_out),
+            strides(Q_out), _ptr(K_out), strides(K_out), s)
+    _check(st, "sol_attn_rope")
+    return Q_out, K_out

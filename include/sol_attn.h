@@ -336,6 +336,110 @@ sol_status sol_attn_fwd_host(const void* Q, const void* K, const void* V, void* 
                              int heads_per_chunk, float* density, void* scratch, size_t scratch_bytes,
                              void* stream);
 
+/* ---- Dense operators around the attention -------------------------------------------------------
+ * The pages list them beside the attention (Sol-Engine README, "The five acceleration methods":
+ * kernel fusion of the memory-bound DiT glue; the review page of the Sol Video Inference Engine
+ * paper names GEMM+GELU, GEMM+residual, fused RoPE+norm and fused AdaLN) and print no formulas; the
+ * definitions below are this library's. They follow the conventions above; where a call accepts
+ * strides or smaller alignments, it says so. Outputs must not overlap inputs unless stated. */
+
+typedef enum { SOL_NORM_NONE = 0, SOL_NORM_LAYER = 1, SOL_NORM_RMS = 2 } sol_norm;
+
+/* Gated residual and norm, the step between two halves of a transformer block, in one pass:
+ *   u  = y, or norm_post(y) * post_gain        x' = res_scale * x + gate[b] * u
+ *   h  = norm(x') * gain * (1 + scale[b]) + shift[b]
+ * over the C channels of each of the B*T rows; layer: (v - mean) / sqrt(var + eps), rms:
+ * v / sqrt(mean v^2 + eps). h is formed from the unrounded x'. A null vector is absent (a factor of
+ * 1, a shift of 0); y null: no residual step, h from x.
+ *   x, y             device, [B, T, C] in dtype `dt`; y may be NULL
+ *   gate, scale,     device, float32: B rows of C, the given number of floats apart (rows of one
+ *   shift            modulation buffer, or 0 for one row shared by all b), or NULL
+ *   gain, post_gain  device, float32 [C], or NULL; post_gain needs post_norm
+ *   norm             SOL_NORM_LAYER or SOL_NORM_RMS; post_norm may also be SOL_NORM_NONE
+ *   x_out            device, out, [B, T, C]: x', exactly where y is given; may be x itself
+ *   h                device, out, [B, T, C]
+ * Any C from 1 to 8192; multiples of 8 (SOL_BF16) or 4 (SOL_F32) with vectors on 16-byte addresses
+ * run with 16-byte accesses, others with single ones. B*T < 2^31. Vectors need 4-byte alignment. */
+sol_status sol_attn_residual_norm(const void* x, const void* y, const float* gate, int64_t gate_stride,
+                                  const float* gain, const float* scale, int64_t scale_stride,
+                                  const float* shift, int64_t shift_stride, const float* post_gain,
+                                  sol_dtype dt, sol_norm norm, sol_norm post_norm, float res_scale,
+                                  float eps, int B, int T, int C, void* x_out, void* h, void* stream);
+
+/* Bytes of device workspace sol_attn_residual_norm_bwd needs for the gradients of vectors (0 for
+ * invalid sizes); no zeroing needed. */
+size_t sol_attn_residual_norm_bwd_workspace_bytes(int B, int T, int C);
+
+/* Gradients of sol_attn_residual_norm, from the forward's inputs alone (x' and the statistics are
+ * formed again).
+ *   dh               device, [B, T, C]: gradient of h
+ *   dx_out           device, [B, T, C] or NULL: gradient that reaches x' from elsewhere (needs y)
+ *   dx, dy           device, out, [B, T, C]; dy exactly where y is given
+ *   dgate, dscale,   device, out, float32 [B, C] contiguous, or NULL where not wanted. Where the
+ *   dshift           forward shared one row (stride 0), each b's share is written
+ *   dgain, dpost_gain  device, out, float32 [C], or NULL where not wanted
+ *   workspace        for any gradient of a vector; may be NULL otherwise
+ * Sums over rows are fp32 in a fixed order: the same inputs give the same bits. B <= 65535, other
+ * arguments and limits as for the forward. */
+sol_status sol_attn_residual_norm_bwd(const void* dh, const void* dx_out, const void* x, const void* y,
+                                      const float* gate, int64_t gate_stride, const float* gain,
+                                      const float* scale, int64_t scale_stride, const float* post_gain,
+                                      sol_dtype dt, sol_norm norm, sol_norm post_norm, float res_scale,
+                                      float eps, int B, int T, int C, void* dx, void* dy, float* dgate,
+                                      float* dgain, float* dscale, float* dshift, float* dpost_gain,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
+typedef enum { SOL_ROPE_INTERLEAVED = 0, SOL_ROPE_HALF = 1 } sol_rope_layout;
+typedef enum { SOL_ROPE_PLAIN = 0, SOL_ROPE_LINEAR = 1, SOL_ROPE_NTK = 2, SOL_ROPE_YARN = 3 } sol_rope_scaling;
+
+/* Angular step per position of each of the rot / 2 pairs, on the HOST. The pairs are split over
+ * `axes` (1 to 4) position axes, sections[a] consecutive pairs each (their sum rot / 2; sections
+ * may be NULL for one axis). Pair j of an axis of n pairs has f = base^(-j / n), and for contexts
+ * `factor` times longer than the trained one:
+ *   SOL_ROPE_LINEAR  f / factor
+ *   SOL_ROPE_NTK     base * factor^(n / (n - 1)) in place of base: the slowest pair stretches by
+ *                    factor, the fastest not at all
+ *   SOL_ROPE_YARN    f (k + (1 - k) / factor), k = clamp((r - turns_low) / (turns_high - turns_low))
+ *                    to [0, 1] with r = original_length f / 2 pi, the pair's turns over the trained
+ *                    context; *attn_factor = 0.1 ln(factor) + 1 (1 for the others), which the
+ *                    calls below put on cosine and sine
+ *   inv_freq     HOST, out, double [rot / 2]; attn_factor HOST, out. Copy inv_freq to the device once. */
+sol_status sol_attn_rope_inv_freq(int rot, double base, int axes, const int* sections,
+                                  sol_rope_scaling scaling, double factor, double original_length,
+                                  double turns_low, double turns_high, double* inv_freq,
+                                  float* attn_factor);
+
+/* Cosine and sine tables, the rope_cos / rope_sin of sol_attn_qknorm_rope_pool (rot = d there):
+ * attn_factor * cos and sin of pos[axis(i)][t] * inv_freq[i], angles formed in 64 bits.
+ *   pos          device, int32 [axes, L]
+ *   sections     HOST, int [axes], or NULL for one axis
+ *   inv_freq     device, double [rot / 2]
+ *   rope_cos/sin device, out, float32 [L, rot / 2] */
+sol_status sol_attn_rope_tables(const int32_t* pos, int axes, const int* sections,
+                                const double* inv_freq, float attn_factor, int L, int rot,
+                                float* rope_cos, float* rope_sin, void* stream);
+
+/* Rotary positions of queries and keys in one pass. Each pair (a, b) of the first `rot` of d channels
+ * becomes attn_factor (a cos - b sin, a sin + b cos); channels from rot on pass through. Pairs are
+ * (2i, 2i + 1) or, SOL_ROPE_HALF, (i, i + rot / 2). inverse != 0 turns back by the same angle with
+ * the same factor: the gradient of the input from that of the output.
+ *   Q, K         device, [B, Hq, L, d] and [B, Hk, L, d] in dtype `dt`, with strides (in elements)
+ *                q_strides = {b, h, l} on the HOST, channels contiguous; strides may be 0 (shared).
+ *                Hk = 0: no keys
+ *   Q_out, K_out device, out, same shapes, strides of their own (at least d). In place (the same
+ *                pointer) the strides must agree. Token-major projections in, head-major tensors
+ *                out, or back for a gradient, need no copy of their own
+ *   pos          device, int32 [axes, L] per batch entry, pos_stride_b elements apart (0: shared)
+ *   sections, inv_freq, attn_factor as above
+ * Even d <= 512, any even rot <= d. 16-byte accesses where addresses, strides, d and (half layout)
+ * rot / 2 allow them, single ones elsewhere. B <= 65535, Hq + Hk <= 65535. */
+sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides,
+                         sol_dtype dt, const int32_t* pos, int64_t pos_stride_b, int axes,
+                         const int* sections, const double* inv_freq, float attn_factor,
+                         sol_rope_layout layout, int inverse, int B, int Hq, int Hk, int L, int d, int rot,
+                         void* Q_out, const int64_t* q_out_strides, void* K_out,
+                         const int64_t* k_out_strides, void* stream);
+
 /* Test hook for the failure-detection path. mode 0 (default) = normal operation. mode 1 makes
  * the next sol_attn_fwd launch (SOL_BF16 path) skip one K-tile load, so the consumer's bounded
  * wait expires: the launch returns early, sets the device error word, and
