@@ -1,5 +1,5 @@
 // C ABI of the dense operators around the attention (declared in include/sol_attn.h): gated
-// residual and norm, rotary positions. Arguments are checked on the host before anything is
+// residual and norm, rotary positions, linear layer. Arguments are checked on the host before anything is
 // launched; nothing here allocates device memory.
 #include <climits>
 #include <cmath>
@@ -88,6 +88,58 @@ sol_status rope_sections(int rot, int axes, const int* sections, int (&end)[4]) 
   if (sum != rot / 2) return fail(SOL_EINVAL, "sections must add up to rot / 2 = %d (they give %lld)", rot / 2, sum);
   return SOL_OK;
 }
+
+// 2-D bf16 view [rows][inner] with boxes of box_inner x box_rows; what lies outside reads as zero and
+// is not written.
+sol_status make_map2d(CUtensorMap* m, const void* base, int inner, int rows, int box_inner, int box_rows,
+                      CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return fail(SOL_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * 2};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SOL_ECUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return SOL_OK;
+}
+
+// An operand of a product with `rows` rows and `inner` columns in memory: K-major tiles of tile_rows
+// rows x 64, or MN-major boxes of 64 x 64.
+sol_status make_operand_map(CUtensorMap* m, const void* base, int rows, int inner, bool mn, int tile_rows) {
+  return make_map2d(m, base, inner, rows, 64, mn ? 64 : tile_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// out [Mo, No] = A . B over Ko, by tiles of 128 x tile_n. A lies in memory as [Mo, Ko] or, a_mn, as
+// [Ko, Mo]; B as [No, Ko] or, b_mn, as [Ko, No].
+sol_status run_gemm(sol::GemmArgs& a, const void* A, const void* Bm, void* out, void* z, cudaStream_t stream) {
+  a.tile_n = sol::linear_tile_n(a.Mo, a.No, a.num_sms);
+  a.store_z = z != nullptr;
+  sol_status st;
+  if ((st = make_operand_map(&a.maps[0], A, a.a_mn ? a.Ko : a.Mo, a.a_mn ? a.Mo : a.Ko, a.a_mn, 128)) != SOL_OK) return st;
+  if ((st = make_operand_map(&a.maps[1], Bm, a.b_mn ? a.Ko : a.No, a.b_mn ? a.No : a.Ko, a.b_mn, a.tile_n)) != SOL_OK) return st;
+  if ((st = make_map2d(&a.maps[2], out, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK) return st;
+  if ((st = make_map2d(&a.maps[3], z != nullptr ? z : out, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK) return st;
+  const cudaError_t e = sol::launch_linear_gemm(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "linear layer launch");
+  return SOL_OK;
+}
+
+sol_status linear_sizes(int M, int N, int K, sol_activation act) {
+  if (act < SOL_ACT_NONE || act > SOL_ACT_SILU) return fail(SOL_EINVAL, "unknown activation %d", static_cast<int>(act));
+  if (!size_ok(M, 1 << 28) || !size_ok(N, 1 << 28) || !size_ok(K, 1 << 28))
+    return fail(SOL_EINVAL, "sizes must be positive (M=%d N=%d K=%d)", M, N, K);
+  if (N % 8 != 0 || K % 8 != 0) return fail(SOL_EUNSUPPORTED, "the linear layer needs N and K in multiples of 8 (N=%d K=%d)", N, K);
+  const long long m = (M + 127) / 128, n = (N + 63) / 64, k = (K + 63) / 64;
+  if (m * n >= (1ll << 31) || ((M + 63ll) / 64) * k >= (1ll << 31) || n * k >= (1ll << 31))
+    return fail(SOL_EUNSUPPORTED, "too many tiles (M=%d N=%d K=%d)", M, N, K);
+  return SOL_OK;
+}
+
+constexpr size_t kErrorBytes = 256;  // the workspace's error words, as sol_attn_check_device_error reads them
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -301,6 +353,105 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
   a.bf16 = dt == SOL_BF16;
   const cudaError_t e = sol::launch_rope(a, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
+  return SOL_OK;
+}
+
+sol_status sol_attn_linear(const void* x, const void* w, const float* bias, const void* residual, sol_activation act, int M,
+                           int N, int K, void* out, void* z, void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  sol_status st = linear_sizes(M, N, K, act);
+  if (st != SOL_OK) return st;
+  if (x == nullptr || w == nullptr || out == nullptr) return fail(SOL_EINVAL, "x, w and out must be non-null");
+  const void* ptrs[] = {x, w, bias, residual, out, z, workspace};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return fail(SOL_EINVAL, "device pointers must be 16-byte aligned");
+  if (workspace != nullptr && ws_bytes < kErrorBytes) return fail(SOL_EINVAL, "workspace too small (%zu < %zu bytes)", ws_bytes, kErrorBytes);
+  int sms = 0;
+  if ((st = current_device(&sms)) != SOL_OK) return st;
+  if (M <= sol::kFewRows) {
+    sol::FewArgs a;
+    if ((st = make_operand_map(&a.maps[0], w, N, K, false, 128)) != SOL_OK) return st;
+    if ((st = make_operand_map(&a.maps[1], x, M, K, false, sol::linear_few_tile(M))) != SOL_OK) return st;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.bias = bias;
+    a.residual = residual;
+    a.out = out;
+    a.z = z;
+    a.act = act;
+    a.ws = static_cast<uint32_t*>(workspace);
+    a.num_sms = sms;
+    const cudaError_t e = sol::launch_linear_few(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "linear layer launch");
+    return SOL_OK;
+  }
+  sol::GemmArgs a;
+  a.Mo = M;
+  a.No = N;
+  a.Ko = K;
+  a.a_mn = a.b_mn = false;
+  a.bias = bias;
+  a.residual = residual;
+  a.act = act;
+  a.ws = static_cast<uint32_t*>(workspace);
+  a.num_sms = sms;
+  return run_gemm(a, x, w, out, z, static_cast<cudaStream_t>(stream));
+}
+
+size_t sol_attn_linear_bwd_workspace_bytes(int M, int N, sol_activation act) {
+  if (!size_ok(M, 1 << 28) || !size_ok(N, 1 << 28) || act < SOL_ACT_NONE || act > SOL_ACT_SILU) return 0;
+  return kErrorBytes + round256(static_cast<size_t>(sol::linear_dz_chunks(M, N)) * N * 4) +
+         (act == SOL_ACT_NONE ? 0 : round256(static_cast<size_t>(M) * N * 2));
+}
+
+sol_status sol_attn_linear_bwd(const void* dy, const void* x, const void* w, const void* z, sol_activation act, int M, int N,
+                               int K, void* dx, void* dw, float* db, void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  sol_status st = linear_sizes(M, N, K, act);
+  if (st != SOL_OK) return st;
+  if (dy == nullptr || workspace == nullptr) return fail(SOL_EINVAL, "dy and workspace must be non-null");
+  if (dx == nullptr && dw == nullptr && db == nullptr) return fail(SOL_EINVAL, "no gradient is wanted: dx, dw and db are all null");
+  if (dx != nullptr && w == nullptr) return fail(SOL_EINVAL, "dx needs w");
+  if (dw != nullptr && x == nullptr) return fail(SOL_EINVAL, "dw needs x");
+  if ((act != SOL_ACT_NONE) != (z != nullptr)) return fail(SOL_EINVAL, "z must be given exactly where there is an activation");
+  const void* ptrs[] = {dy, x, w, z, dx, dw, workspace};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return fail(SOL_EINVAL, "device pointers must be 16-byte aligned");
+  if (!aligned_to(db, 4)) return fail(SOL_EINVAL, "db must be 4-byte aligned");
+  const size_t need = sol_attn_linear_bwd_workspace_bytes(M, N, act);
+  if (ws_bytes < need) return fail(SOL_EINVAL, "workspace too small (%zu < %zu bytes)", ws_bytes, need);
+  int sms = 0;
+  if ((st = current_device(&sms)) != SOL_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kErrorBytes);
+  void* dz = static_cast<uint8_t*>(workspace) + kErrorBytes + round256(static_cast<size_t>(sol::linear_dz_chunks(M, N)) * N * 4);
+  if (act != SOL_ACT_NONE || db != nullptr) {
+    const cudaError_t e = sol::launch_linear_dz(dy, z, act, M, N, dz, db != nullptr ? part : nullptr, db, s);
+    if (e != cudaSuccess) return cuda_fail(e, "activation gradient launch");
+  }
+  const void* g = act != SOL_ACT_NONE ? dz : dy;
+  sol::GemmArgs a;
+  a.bias = nullptr;
+  a.residual = nullptr;
+  a.act = sol::ACT_NONE;
+  a.ws = static_cast<uint32_t*>(workspace);
+  a.num_sms = sms;
+  if (dx != nullptr) {
+    a.Mo = M;
+    a.No = K;
+    a.Ko = N;
+    a.a_mn = false;
+    a.b_mn = true;
+    if ((st = run_gemm(a, g, w, dx, nullptr, s)) != SOL_OK) return st;
+  }
+  if (dw != nullptr) {
+    a.Mo = N;
+    a.No = K;
+    a.Ko = M;
+    a.a_mn = a.b_mn = true;
+    if ((st = run_gemm(a, g, x, dw, nullptr, s)) != SOL_OK) return st;
+  }
   return SOL_OK;
 }
 

@@ -186,6 +186,42 @@ struct RopeTableArgs {
 };
 cudaError_t launch_rope_tables(const RopeTableArgs& a, cudaStream_t stream);
 
+// Linear layer (sol_attn_linear) and its gradients: bf16 operands, fp32 accumulation.
+enum : int { ACT_NONE = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_SILU = 3 };
+constexpr int kFewRows = 128;  // up to here the forward takes the kernel for few rows
+constexpr int kDzBlocks = 1184;  // blocks of the dz pass: 8 per SM
+int linear_tile_n(int Mo, int No, int num_sms);  // output columns per tile: 256, 128 or 64
+int linear_few_tile(int M);                      // tokens per tile of the kernel for few rows
+int linear_dz_chunks(int M, int N);              // row blocks of the dz pass, one partial column sum each
+struct GemmArgs {
+  CUtensorMap maps[4];  // A, B (boxes as launch_linear_gemm's tiles want them), out, z
+  int Mo, No, Ko;       // output rows, columns, reduction
+  bool a_mn, b_mn;      // operand is MN-major: its memory rows run along M or N
+  int tile_n;
+  const float* bias;    // [No] or null
+  const void* residual; // bf16 [Mo, No] or null
+  int act;
+  bool store_z;
+  uint32_t* ws;         // error words or null
+  int num_sms;
+};
+cudaError_t launch_linear_gemm(const GemmArgs& a, cudaStream_t stream);
+struct FewArgs {
+  CUtensorMap maps[2];  // w, x
+  int M, N, K;
+  const float* bias;
+  const void* residual;
+  void* out;
+  void* z;  // or null
+  int act;
+  uint32_t* ws;
+  int num_sms;
+};
+cudaError_t launch_linear_few(const FewArgs& a, cudaStream_t stream);
+// dz = dy act'(z) (z null: dz = dy, not written) and, with part and db, the column sums of dz.
+cudaError_t launch_linear_dz(const void* dy, const void* z, int act, int M, int N, void* dz, float* part, float* db,
+                             cudaStream_t stream);
+
 // bf16, d in {64, 128}, block 128: routing pass for every unit (q_bar kernel, then the routing
 // kernel); writes a.route_qbar, a.route_bits, the optional mask and the per-head kept counts
 // (ws + WS_COUNTS).

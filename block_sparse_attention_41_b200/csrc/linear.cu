@@ -1,0 +1,721 @@
+// Linear layer out = residual + act(x w^T + bias) and its gradients on the 5th-generation tensor
+// cores (bf16 operands, fp32 accumulation in tensor memory).
+//
+// One kernel serves the three products, since each operand tile may be K-major (the reduction runs
+// along its rows) or MN-major (the reduction runs down its columns), which the shared-memory
+// descriptors express without a transpose:
+//   out [M, N] = x [M, K] . w [N, K]^T    both K-major
+//   dx  [M, K] = dz [M, N] . w [N, K]     dz K-major, w MN-major
+//   dw  [N, K] = dz [M, N]^T . x [M, K]   both MN-major
+//
+// Bound by the tensor pipe for many rows. A persistent CTA per SM walks 128 x TN output tiles; one
+// warp issues TMA loads into a ring of 64-deep slices, one issues the MMAs, eight turn accumulators
+// into outputs. The accumulator is double-buffered in tensor memory, so the epilogue of one tile
+// (bias, activation, residual, rounding, and a TMA store per warp out of swizzled shared memory)
+// runs under the products of the next. TN is 256, 128 or 64: the widest tile moves the fewest
+// operand bytes per product, a narrower one fills the SMs when there are few tiles.
+//
+// With up to kFewRows rows the layer is bound by reading w once. There the product is taken
+// transposed: 128 rows of w are the M side of the MMA and the tokens its N side, so the ring holds
+// almost nothing but w. The reduction is split over the CTAs of a cluster to have enough loads in
+// flight, and the cluster adds its fp32 partial tiles over distributed shared memory in rank order,
+// so no workspace and no atomics are needed and the bits do not depend on timing.
+//
+// Every wait is bounded: on expiry the CTA records the timeout in the caller's workspace (where one
+// is given), lets its copies and MMAs in flight end, frees its tensor memory and returns.
+#include <cmath>
+
+#include "device_common.cuh"
+#include "launchers.h"
+
+namespace sol {
+
+namespace {
+
+constexpr int BM = 128;            // output rows per tile
+constexpr int BK = 64;             // reduction depth per slice: one 128-byte swizzle row of bf16
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr int kEpiBuf = 32 * 64;   // one warp's staging buffer: 32 rows x 32 bf16 columns
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kGroupM = 16;        // output row tiles walked together, so a wave of tiles is about square
+
+template <int TN>
+struct GemmCfg {
+  static constexpr int A_BYTES = BM * BK * 2;
+  static constexpr int B_BYTES = TN * BK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int NS = 196608 / STAGE;  // 4, 6 or 8 slices of 48, 32 or 24 KB
+  static constexpr int OFF_EPI = NS * STAGE;
+  static constexpr int OFF_BAR = OFF_EPI + kEpiWarps * 2 * kEpiBuf;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // + alignment of the ring to 1024 bytes
+  static constexpr int TMEM_COLS = 2 * TN;
+};
+
+struct GemmParams {
+  int Mo, No, nk;  // output rows and columns, reduction slices
+  int tiles_m, tiles_n;
+  const float* bias;               // [No] or null
+  const __nv_bfloat16* residual;   // [Mo, No] or null
+  int act;
+  int store_z;
+  uint32_t* ws;  // error words, or null
+};
+
+// ---- activations and their slopes -----------------------------------------------------------------
+// tanh-form gelu: z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3). With e = 2^(-2 u log2 e), both
+// ends are right without a branch: e = inf gives 0, e = 0 gives z.
+__device__ __forceinline__ float sigmoid_of(float x) { return __fdividef(1.0f, 1.0f + ex2_approx(-1.4426950408889634f * x)); }
+// __fdividef(1, d) is 0 for d above 2^126, which is what the sigmoid tends to there.
+
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case ACT_GELU_TANH: return z * sigmoid_of(1.5957691216057308f * fmaf(0.044715f * z * z, z, z));
+    case ACT_SILU: return z * sigmoid_of(z);
+    default: return z;
+  }
+}
+__device__ __forceinline__ float activation_slope(float z, int act) {
+  switch (act) {
+    case ACT_GELU:
+      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
+             z * 0.39894228040143268f * ex2_approx(-0.72134752044448170f * z * z);
+    case ACT_GELU_TANH: {
+      const float z2 = z * z;
+      const float s = sigmoid_of(1.5957691216057308f * fmaf(0.044715f * z2, z, z));
+      return s + z * s * (1.0f - s) * 1.5957691216057308f * fmaf(3.0f * 0.044715f, z2, 1.0f);
+    }
+    case ACT_SILU: {
+      const float s = sigmoid_of(z);
+      return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    default: return 1.0f;
+  }
+}
+
+// ---- small PTX helpers of this file -----------------------------------------------------------------
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+               ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_wait() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Records an expired wait: stops the CTA's other roles and, where there is a workspace, tells the host.
+__device__ __forceinline__ void report(volatile int* abort_flag, uint32_t* ws, uint32_t where) {
+  if (ws != nullptr) raise_timeout(abort_flag, ws, where);
+  else *abort_flag = 1;
+}
+
+constexpr uint32_t instr_desc(int N, bool a_mn, bool b_mn) {
+  return idesc_bf16_f32(BM, N, b_mn) | (a_mn ? 1u << 15 : 0u);
+}
+
+// One 64-deep slice of an operand: `rows` rows along its M or N side, starting at r0, reduction from
+// k0. K-major: one box of 64 x rows. MN-major: boxes of 64 (M or N) x 64 (reduction), 8 KB each.
+template <bool MN>
+__device__ __forceinline__ void load_operand(uint32_t dst, const void* tmap, uint32_t bar, int r0, int rows, int k0) {
+  if constexpr (!MN) {
+    tma_load_2d(dst, tmap, bar, k0, r0);
+  } else {
+    for (int i = 0; i < rows / 64; ++i) tma_load_2d(dst + i * 8192, tmap, bar, r0 + 64 * i, k0);
+  }
+}
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+  return MN ? smem_desc_sw128(saddr, 8192, 1024) : smem_desc_sw128(saddr, 16, 1024);
+}
+// descriptor step of 16 reduction elements: 32 bytes along a row, or 16 rows of 128 bytes
+template <bool MN>
+constexpr uint32_t kDescStep = MN ? 2048 >> 4 : 32 >> 4;
+
+// Tile number -> (row tile, column tile): kGroupM row tiles at a time, column by column.
+__device__ __forceinline__ void tile_of(const GemmParams& p, int t, int& tm, int& tn) {
+  const int per_group = kGroupM * p.tiles_n;
+  const int g = t / per_group, in = t - g * per_group;
+  const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
+  tm = g * kGroupM + in % rows;
+  tn = in / rows;
+}
+
+// ---- many rows ------------------------------------------------------------------------------------
+template <int TN, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    sol_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
+                      const __grid_constant__ GemmParams p) {
+  using C = GemmCfg<TN>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sb - raw);
+  const uint32_t bars = sb + C::OFF_BAR;
+  const uint32_t bar_full = bars, bar_empty = bars + 8 * C::NS, bar_acc = bars + 16 * C::NS,
+                 bar_free = bar_acc + 16, bar_drain = bar_free + 16;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 16 * C::NS + 40);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 16 * C::NS + 44);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar_acc + 8 * a, 1);
+      mbar_init(bar_free + 8 * a, kEpiWarps);
+    }
+    mbar_init(bar_drain, 1);
+    fence_mbar_init();
+    *s_abort = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int tiles = p.tiles_m * p.tiles_n;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_a);
+      tma_prefetch_desc(&map_b);
+      uint32_t g = 0;  // slices loaded so far
+      int w = WAIT_OK;
+      for (int t = blockIdx.x; t < tiles && w == WAIT_OK; t += gridDim.x) {
+        int tm, tn;
+        tile_of(p, t, tm, tn);
+        for (int k = 0; k < p.nk; ++k, ++g) {
+          const uint32_t s = g % C::NS;
+          if (g >= C::NS) {
+            w = mbar_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort, kWaitLimitNs);
+            if (w != WAIT_OK) break;
+          }
+          mbar_arrive_expect_tx(bar_full + 8 * s, C::STAGE);
+          const uint32_t dst = sb + s * C::STAGE;
+          load_operand<A_MN>(dst, &map_a, bar_full + 8 * s, tm * BM, BM, k * BK);
+          load_operand<B_MN>(dst + C::A_BYTES, &map_b, bar_full + 8 * s, tn * TN, TN, k * BK);
+        }
+      }
+      if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_PRODUCER);
+      // no copy may be in flight when shared memory is released: the last use of every slice
+      for (uint32_t i = g > C::NS ? g - C::NS : 0; i < g; ++i)
+        mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = instr_desc(TN, A_MN, B_MN);
+      const uint64_t da0 = operand_desc<A_MN>(sb), db0 = operand_desc<B_MN>(sb + C::A_BYTES);
+      uint32_t g = 0, it = 0;
+      int w = WAIT_OK;
+      for (int t = blockIdx.x; t < tiles && w == WAIT_OK; t += gridDim.x, ++it) {
+        const uint32_t acc = it & 1u;
+        if (it >= 2) {
+          w = mbar_wait(bar_free + 8 * acc, (it / 2 - 1u) & 1u, s_abort, kWaitLimitNs);
+          if (w != WAIT_OK) break;
+          tc_fence_after();
+        }
+        for (int k = 0; k < p.nk; ++k, ++g) {
+          const uint32_t s = g % C::NS;
+          w = mbar_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort, kWaitLimitNs);
+          if (w != WAIT_OK) break;
+          tc_fence_after();
+          const uint64_t da = da0 + ((s * C::STAGE) >> 4), db = db0 + ((s * C::STAGE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_bf16_ss(tmem + acc * TN, da + kk * kDescStep<A_MN>, db + kk * kDescStep<B_MN>, idesc,
+                        (k > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(bar_empty + 8 * s);
+        }
+        if (w == WAIT_OK) tc_commit(bar_acc + 8 * acc);
+      }
+      if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_MMA);
+      tc_commit(bar_drain);  // no MMA may be in flight when tensor memory is freed
+      mbar_wait(bar_drain, 0, nullptr, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else {
+    const int ew = warp - 2, q = warp & 3, side = ew >> 2;  // TMEM lanes 32 q.., column half
+    const int c_lo = side * (TN / 2);
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t buf0 = sb + C::OFF_EPI + ew * 2 * kEpiBuf;
+    const uint32_t swz = (lane >> 1) & 3;  // 64-byte swizzle: 16-byte chunk c of row r sits at c ^ ((r / 2) % 4)
+    uint32_t it = 0, stores = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+      int tm, tn;
+      tile_of(p, t, tm, tn);
+      const uint32_t acc = it & 1u;
+      const int w = mbar_wait(bar_acc + 8 * acc, (it / 2) & 1u, s_abort, kWaitLimitNs);
+      if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
+      if (__any_sync(0xffffffffu, w != WAIT_OK)) break;
+      tc_fence_after();
+      const int row0 = tm * BM + q * 32, row = row0 + lane;
+      const bool live = row < p.Mo;
+#pragma unroll 1
+      for (int c = c_lo; c < c_lo + TN / 2; c += 32) {
+        const int col0 = tn * TN + c;
+        if (col0 >= p.No) break;  // uniform: the rest of the tile is past the last column
+        uint32_t r[32];
+        tmem_ld_x32(tmem + lane_base + acc * TN + c, r);
+        auto emit = [&](const CUtensorMap* map, const uint32_t (&pk)[16]) {
+          const uint32_t buf = buf0 + (stores & 1u) * kEpiBuf;
+          if (lane == 0) bulk_wait_read<1>();  // the store before the last one has left this buffer
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((v ^ swz) << 4)),
+                         "r"(pk[4 * v]), "r"(pk[4 * v + 1]), "r"(pk[4 * v + 2]), "r"(pk[4 * v + 3])
+                         : "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.Mo) tma_store_2d(map, buf, col0, row0);  // rows and columns past the end are not written
+            bulk_commit();
+          }
+          ++stores;
+        };
+        uint32_t pk[16];
+        if (p.bias != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            if (col0 + j < p.No) {  // No is a multiple of 8
+              const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col0 + j));
+              r[j] = __float_as_uint(__uint_as_float(r[j]) + b.x);
+              r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) + b.y);
+              r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) + b.z);
+              r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) + b.w);
+            }
+          }
+        }
+        if (p.store_z) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+          emit(&map_z, pk);
+        }
+        if (p.act != ACT_NONE) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(activate(__uint_as_float(r[j]), p.act));
+        }
+        if (p.residual != nullptr && live) {
+          const __nv_bfloat16* res = p.residual + static_cast<size_t>(row) * p.No + col0;
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (col0 + j < p.No) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(res + j));
+              const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                r[j + 2 * i] = __float_as_uint(__uint_as_float(r[j + 2 * i]) + __uint_as_float(wv[i] << 16));
+                r[j + 2 * i + 1] = __float_as_uint(__uint_as_float(r[j + 2 * i + 1]) + __uint_as_float(wv[i] & 0xffff0000u));
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        emit(&map_out, pk);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_free + 8 * acc);
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// ---- few rows --------------------------------------------------------------------------------------
+constexpr int kFewThreads = 192;
+
+template <int TT>
+struct FewCfg {
+  static constexpr int A_BYTES = BM * BK * 2;  // 128 rows of w
+  static constexpr int B_BYTES = TT * BK * 2;  // TT tokens
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int NS = 6;
+  static constexpr int PART = TT * BM * 4;     // fp32 partial tile [token][row of w], over the ring once it is done
+  static constexpr int RING = NS * STAGE > PART ? NS * STAGE : PART;
+  static constexpr int OFF_BAR = RING;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int TMEM_COLS = TT < 32 ? 32 : TT;
+};
+
+struct FewParams {
+  int M, N, nk;
+  int split;  // CTAs of a cluster, each with its share of the reduction
+  const float* bias;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* out;
+  __nv_bfloat16* z;
+  int act;
+  uint32_t* ws;
+};
+
+template <int TT>
+__global__ void __launch_bounds__(kFewThreads)
+    sol_linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                          const __grid_constant__ FewParams p) {
+  using C = FewCfg<TT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sb - raw);
+  const uint32_t bar_full = sb + C::OFF_BAR, bar_empty = bar_full + 8 * C::NS, bar_acc = bar_empty + 8 * C::NS;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 16 * C::NS + 8);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 16 * C::NS + 12);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int n0 = blockIdx.x / p.split * BM;
+  const int k_lo = static_cast<int>(static_cast<long long>(p.nk) * rank / p.split);
+  const int k_hi = static_cast<int>(static_cast<long long>(p.nk) * (rank + 1) / p.split);  // split <= nk: at least one slice
+  if (tid == 0) {
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    mbar_init(bar_acc, 1);
+    fence_mbar_init();
+    *s_abort = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  bool ok = true;  // of the epilogue warps: the accumulator is complete
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t g = 0;
+      int w = WAIT_OK;
+      for (int k = k_lo; k < k_hi; ++k, ++g) {
+        const uint32_t s = g % C::NS;
+        if (g >= C::NS) {
+          w = mbar_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort, kWaitLimitNs);
+          if (w != WAIT_OK) break;
+        }
+        mbar_arrive_expect_tx(bar_full + 8 * s, C::STAGE);
+        tma_load_2d(sb + s * C::STAGE, &map_w, bar_full + 8 * s, k * BK, n0);
+        tma_load_2d(sb + s * C::STAGE + C::A_BYTES, &map_x, bar_full + 8 * s, k * BK, 0);
+      }
+      if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_PRODUCER);
+      for (uint32_t i = g > C::NS ? g - C::NS : 0; i < g; ++i)
+        mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = instr_desc(TT, false, false);
+      const uint64_t da0 = operand_desc<false>(sb), db0 = operand_desc<false>(sb + C::A_BYTES);
+      uint32_t g = 0;
+      int w = WAIT_OK;
+      for (int k = k_lo; k < k_hi; ++k, ++g) {
+        const uint32_t s = g % C::NS;
+        w = mbar_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort, kWaitLimitNs);
+        if (w != WAIT_OK) break;
+        tc_fence_after();
+        const uint64_t da = da0 + ((s * C::STAGE) >> 4), db = db0 + ((s * C::STAGE) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          mma_bf16_ss(tmem, da + kk * kDescStep<false>, db + kk * kDescStep<false>, idesc, (g > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(bar_empty + 8 * s);
+      }
+      if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_MMA);
+      tc_commit(bar_acc);  // also after an abort: the MMAs in flight end before tensor memory is freed
+      mbar_wait(bar_acc, 0, nullptr, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else {
+    const int w = mbar_wait(bar_acc, 0, nullptr, 2 * kWaitLimitNs);
+    if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
+    ok = !__any_sync(0xffffffffu, w != WAIT_OK);
+    if (ok) {
+      tc_fence_after();
+      // every slice has been read by the MMAs, so the partial tile may take the ring's place
+      const int q = warp & 3, n = q * 32 + lane;
+      float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int c = 0; c < TT; c += 16) {
+        if (c >= p.M) break;
+        uint32_t r[16];
+        tmem_ld_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * BM + n] = __uint_as_float(r[j]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+  const bool aborted = *s_abort != 0;
+  if (p.split > 1) cluster_arrive_wait();
+  // each CTA of the cluster finishes an equal share of the M x 128 values (128 is a multiple of split)
+  if (!aborted) {
+    const int share = p.M * BM / p.split;
+    for (int e = rank * share + tid; e < (rank + 1) * share; e += kFewThreads) {
+      const int m = e / BM, n = n0 + (e & (BM - 1));
+      float v = 0.f;
+      if (p.split == 1) {
+        v = reinterpret_cast<const float*>(smem)[e];
+      } else {
+        for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(sb + 4 * e, r);
+      }
+      if (n >= p.N) continue;
+      if (p.bias != nullptr) v += __ldg(p.bias + n);
+      const size_t o = static_cast<size_t>(m) * p.N + n;
+      if (p.z != nullptr) p.z[o] = __float2bfloat16_rn(v);
+      v = activate(v, p.act);
+      if (p.residual != nullptr) v += __bfloat162float(p.residual[o]);
+      p.out[o] = __float2bfloat16_rn(v);
+    }
+  }
+  if (p.split > 1) cluster_arrive_wait();  // no CTA leaves while another reads its partial tile
+}
+
+// ---- gradient of the activation and of the bias --------------------------------------------------------
+// dz = dy act'(z) in bf16 (the operand of the two products that follow; the rounding is theirs), and
+// per block of rows the fp32 column sums of the unrounded dz, added by a second kernel in a fixed
+// order. HBM-bound: 32 threads side by side cover 256 columns with 16-byte vectors, 8 rows at a time.
+constexpr int kDzCols = 256, kDzRows = 8;
+
+struct DzParams {
+  const __nv_bfloat16* dy;
+  const __nv_bfloat16* z;   // null: dz = dy
+  __nv_bfloat16* dz;        // null where dz = dy
+  float* part;              // [chunks, N] or null
+  int M, N, act, rows;      // rows per block
+};
+
+__global__ void __launch_bounds__(kDzCols / 8 * kDzRows) sol_linear_dz_kernel(const __grid_constant__ DzParams p) {
+  __shared__ float s[kDzRows][kDzCols + 8];
+  const int lane = threadIdx.x, ty = threadIdx.y;
+  const int c = blockIdx.x * kDzCols + lane * 8;
+  const int r_lo = blockIdx.y * p.rows, r_hi = min(r_lo + p.rows, p.M);
+  float a[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a[k] = 0.f;
+  if (c < p.N) {
+#pragma unroll 2
+    for (int r = r_lo + ty; r < r_hi; r += kDzRows) {
+      const size_t o = static_cast<size_t>(r) * p.N + c;
+      const uint4 g = __ldg(reinterpret_cast<const uint4*>(p.dy + o));
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(gw[k] << 16);
+        v[2 * k + 1] = __uint_as_float(gw[k] & 0xffff0000u);
+      }
+      if (p.z != nullptr) {
+        const uint4 zz = __ldg(reinterpret_cast<const uint4*>(p.z + o));
+        const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] *= activation_slope(__uint_as_float(zw[k] << 16), p.act);
+          v[2 * k + 1] *= activation_slope(__uint_as_float(zw[k] & 0xffff0000u), p.act);
+        }
+        *reinterpret_cast<uint4*>(p.dz + o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                         pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a[k] += v[k];
+    }
+  }
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[ty][lane * 8 + k] = a[k];
+  __syncthreads();
+  const int i = ty * 32 + lane, col = blockIdx.x * kDzCols + i;  // 256 threads: one column each
+  if (col < p.N) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < kDzRows; ++k) t += s[k][i];
+    p.part[static_cast<size_t>(blockIdx.y) * p.N + col] = t;
+  }
+}
+
+__global__ void __launch_bounds__(512) sol_linear_db_kernel(const float* __restrict__ part, float* __restrict__ db, int N,
+                                                            int chunks) {
+  __shared__ float s[16][33];
+  const int col = blockIdx.x * 32 + threadIdx.x;
+  float a = 0.f;
+  if (col < N) {
+#pragma unroll 4
+    for (int i = threadIdx.y; i < chunks; i += 16) a += part[static_cast<size_t>(i) * N + col];
+  }
+  s[threadIdx.y][threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.y == 0 && col < N) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += s[i][threadIdx.x];
+    db[col] = t;
+  }
+}
+
+template <int TN, bool A_MN, bool B_MN>
+cudaError_t launch_gemm_t(const GemmArgs& a, GemmParams p, cudaStream_t stream) {
+  using C = GemmCfg<TN>;
+  p.tiles_m = (a.Mo + BM - 1) / BM;
+  p.tiles_n = (a.No + TN - 1) / TN;
+  const cudaError_t e = cudaFuncSetAttribute(sol_linear_kernel<TN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+  const int grid = static_cast<int>(tiles < a.num_sms ? tiles : a.num_sms);
+  sol_linear_kernel<TN, A_MN, B_MN><<<grid, kGemmThreads, C::SMEM, stream>>>(a.maps[0], a.maps[1], a.maps[2], a.maps[3], p);
+  return cudaGetLastError();
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t launch_gemm_n(const GemmArgs& a, const GemmParams& p, cudaStream_t stream) {
+  if (a.tile_n == 256) return launch_gemm_t<256, A_MN, B_MN>(a, p, stream);
+  if (a.tile_n == 128) return launch_gemm_t<128, A_MN, B_MN>(a, p, stream);
+  return launch_gemm_t<64, A_MN, B_MN>(a, p, stream);
+}
+
+template <int TT>
+cudaError_t launch_few_t(const FewArgs& a, const FewParams& p, cudaStream_t stream) {
+  using C = FewCfg<TT>;
+  const cudaError_t e = cudaFuncSetAttribute(sol_linear_few_kernel<TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.N + BM - 1) / BM * p.split);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, sol_linear_few_kernel<TT>, a.maps[0], a.maps[1], p);
+}
+
+}  // namespace
+
+int linear_tile_n(int Mo, int No, int num_sms) {
+  // time of the last SM to finish, in columns of a 256-wide tile's rate: a narrower tile re-reads more
+  // operand bytes per product and runs at a lower rate
+  const struct { int tn; double cost; } options[] = {{256, 256.0}, {128, 150.0}, {64, 100.0}};
+  int best = 256;
+  double least = 0.0;
+  for (const auto& o : options) {
+    const double tiles = std::ceil(Mo / 128.0) * std::ceil(No / static_cast<double>(o.tn));
+    const double t = std::ceil(tiles / num_sms) * o.cost;
+    if (o.tn == 256 || t < least) {
+      least = t;
+      best = o.tn;
+    }
+  }
+  return best;
+}
+
+int linear_few_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+int linear_dz_chunks(int M, int N) {
+  const int cols = (N + kDzCols - 1) / kDzCols;
+  const int most = (M + 4 * kDzRows - 1) / (4 * kDzRows);  // at least four rows per thread
+  const int want = (kDzBlocks + cols - 1) / cols;
+  const int rows = (M + (most < want ? most : want) - 1) / (most < want ? most : want);
+  return (M + rows - 1) / rows;
+}
+
+cudaError_t launch_linear_gemm(const GemmArgs& a, cudaStream_t stream) {
+  GemmParams p = {};
+  p.Mo = a.Mo;
+  p.No = a.No;
+  p.nk = (a.Ko + BK - 1) / BK;
+  p.bias = a.bias;
+  p.residual = static_cast<const __nv_bfloat16*>(a.residual);
+  p.act = a.act;
+  p.store_z = a.store_z;
+  p.ws = a.ws;
+  if (a.a_mn) return launch_gemm_n<true, true>(a, p, stream);
+  return a.b_mn ? launch_gemm_n<false, true>(a, p, stream) : launch_gemm_n<false, false>(a, p, stream);
+}
+
+cudaError_t launch_linear_few(const FewArgs& a, cudaStream_t stream) {
+  FewParams p = {};
+  p.M = a.M;
+  p.N = a.N;
+  p.nk = (a.K + BK - 1) / BK;
+  p.bias = a.bias;
+  p.residual = static_cast<const __nv_bfloat16*>(a.residual);
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.z = static_cast<__nv_bfloat16*>(a.z);
+  p.act = a.act;
+  p.ws = a.ws;
+  // the reduction over 1, 2, 4 or 8 CTAs: until there are four CTAs per SM, as long as each keeps 8 slices
+  const int tiles = (a.N + BM - 1) / BM;
+  p.split = 1;
+  while (p.split < 8 && tiles * p.split < 4 * a.num_sms && p.nk / (2 * p.split) >= 8) p.split *= 2;
+  switch (linear_few_tile(a.M)) {
+    case 16: return launch_few_t<16>(a, p, stream);
+    case 32: return launch_few_t<32>(a, p, stream);
+    case 64: return launch_few_t<64>(a, p, stream);
+    default: return launch_few_t<128>(a, p, stream);
+  }
+}
+
+cudaError_t launch_linear_dz(const void* dy, const void* z, int act, int M, int N, void* dz, float* part, float* db,
+                             cudaStream_t stream) {
+  DzParams p;
+  p.dy = static_cast<const __nv_bfloat16*>(dy);
+  p.z = static_cast<const __nv_bfloat16*>(z);
+  p.dz = static_cast<__nv_bfloat16*>(dz);
+  p.part = part;
+  p.M = M;
+  p.N = N;
+  p.act = act;
+  const int chunks = linear_dz_chunks(M, N);
+  p.rows = (M + chunks - 1) / chunks;
+  sol_linear_dz_kernel<<<dim3((N + kDzCols - 1) / kDzCols, chunks), dim3(kDzCols / 8, kDzRows), 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || part == nullptr) return e;
+  sol_linear_db_kernel<<<(N + 31) / 32, dim3(32, 16), 0, stream>>>(part, db, N, chunks);
+  return cudaGetLastError();
+}
+
+}  // namespace sol

@@ -47,11 +47,15 @@ EXPORTED = (
     "sol_attn_rope_inv_freq",
     "sol_attn_rope_tables",
     "sol_attn_rope",
+    "sol_attn_linear",
+    "sol_attn_linear_bwd",
+    "sol_attn_linear_bwd_workspace_bytes",
 )
 
 # names of the enumerations of the dense operators
 NORMS = {"none": 0, "layer": 1, "rms": 2}
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ACTIVATIONS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
@@ -136,6 +140,12 @@ def load_library() -> ctypes.CDLL:
     lib.sol_attn_rope.argtypes = [vp, i64p, vp, i64p, i32, vp, i64, i32, i32p, vp, f32, i32, i32, i32, i32, i32, i32, i32,
                                   i32, vp, i64p, vp, i64p, vp]
     lib.sol_attn_rope.restype = i32
+    lib.sol_attn_linear.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, size, vp]
+    lib.sol_attn_linear.restype = i32
+    lib.sol_attn_linear_bwd_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.sol_attn_linear_bwd_workspace_bytes.restype = size
+    lib.sol_attn_linear_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, size, vp]
+    lib.sol_attn_linear_bwd.restype = i32
     lib.sol_attn_check_device_error.argtypes = [vp, vp]
     lib.sol_attn_check_device_error.restype = i32
     lib.sol_attn_debug_drop_one_load.argtypes = [i32]
@@ -797,3 +807,85 @@ def sol_attn_rope(Q, K, pos, inv_freq, layout: str = "interleaved", sections=Non
             strides(Q_out), _ptr(K_out), strides(K_out), s)
     _check(st, "sol_attn_rope")
     return Q_out, K_out
+
+
+def _check_linear(first: str, a, w, x=None):
+    """Shapes of a product's bf16 operands: leading shape, M, N, K. `a` is x or, with x given apart, dy."""
+    if not isinstance(a, torch.Tensor) or not a.is_cuda:
+        raise TypeError(f"{first} must be a CUDA tensor")
+    for n, t in ((first, a), ("w", w), ("x", x)):
+        if t is None:
+            continue
+        _need_cuda_on(n, t, a.device, torch.bfloat16)
+        if t.dim() < 1 or not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    if w is not None and w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+
+
+def _error_words(workspace, device):
+    if workspace is not None:
+        _need_cuda_on("workspace", workspace, device, torch.uint8)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+
+
+def sol_attn_linear(x, w, bias=None, act: str = "none", residual=None, out=None, z=None, want_z: bool = False,
+                    workspace=None, stream=None):
+    """residual + act(x w^T + bias): x bf16 [..., K], w bf16 [N, K], bias fp32 [N], residual bf16 [..., N];
+    act "none", "gelu", "gelu_tanh" or "silu". Returns out, or (out, z) with z = x w^T + bias (bf16, for
+    sol_attn_linear_bwd) when want_z or a z tensor is given. workspace: a zeroed uint8 tensor of 256
+    bytes or more for sol_attn_check_device_error."""
+    _check_linear("x", x, w)
+    code = _choice("act", act, ACTIVATIONS)
+    N, K = w.shape
+    if x.shape[-1] != K:
+        raise ValueError(f"x must be [..., K] with w's K = {K}, got {tuple(x.shape)}")
+    shape = x.shape[:-1] + (N,)
+    M = 1
+    for n in x.shape[:-1]:
+        M *= n
+    _need_vector("bias", bias, x.device, N)
+    for n, t in (("residual", residual), ("out", out), ("z", z)):
+        if t is not None:
+            _need_cuda_on(n, t, x.device, torch.bfloat16)
+            if t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{n} must be contiguous with shape {tuple(shape)}")
+    _error_words(workspace, x.device)
+    with _On(x.device, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        if z is None and want_z:
+            z = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        st = load_library().sol_attn_linear(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), code, M, N, K, _ptr(out), _ptr(z),
+                                            _ptr(workspace), 0 if workspace is None else workspace.numel(), s)
+    _check(st, "sol_attn_linear")
+    return out if z is None else (out, z)
+
+
+def sol_attn_linear_bwd(dy, x, w, z=None, act: str = "none", want_dx: bool = True, want_dw: bool = True,
+                        want_db: bool = True, workspace=None, stream=None):
+    """Gradients of sol_attn_linear from dy bf16 [..., N], its inputs and, with an activation, the z that it
+    returned. Returns (dx, dw, db), bf16, bf16 and fp32, None where not wanted; residual's is dy."""
+    _check_linear("dy", dy, w, x)
+    code = _choice("act", act, ACTIVATIONS)
+    N, K = w.shape
+    if dy.shape[-1] != N or x.shape != dy.shape[:-1] + (K,):
+        raise ValueError(f"dy must be [..., {N}] and x [..., {K}] with the same rows, got {tuple(dy.shape)} and {tuple(x.shape)}")
+    M = 1
+    for n in dy.shape[:-1]:
+        M *= n
+    if z is not None:
+        _need_like("z", z, dy)
+    _error_words(workspace, dy.device)
+    lib = load_library()
+    with _On(dy.device, stream) as s:
+        dx = torch.empty_like(x) if want_dx else None
+        dw = torch.empty_like(w) if want_dw else None
+        db = torch.empty(N, dtype=torch.float32, device=dy.device) if want_db else None
+        if workspace is None:
+            workspace = torch.empty(lib.sol_attn_linear_bwd_workspace_bytes(M, N, code), dtype=torch.uint8, device=dy.device)
+        st = lib.sol_attn_linear_bwd(_ptr(dy), _ptr(x), _ptr(w), _ptr(z), code, M, N, K, _ptr(dx), _ptr(dw), _ptr(db),
+                                     _ptr(workspace), workspace.numel(), s)
+    _check(st, "sol_attn_linear_bwd")
+    return dx, dw, db

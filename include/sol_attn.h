@@ -440,6 +440,38 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
                          void* Q_out, const int64_t* q_out_strides, void* K_out,
                          const int64_t* k_out_strides, void* stream);
 
+typedef enum { SOL_ACT_NONE = 0, SOL_ACT_GELU = 1, SOL_ACT_GELU_TANH = 2, SOL_ACT_SILU = 3 } sol_activation;
+
+/* Linear layer with its epilogue: z = x w^T + bias, out = residual + act(z). bf16 operands, fp32
+ * accumulation (tcgen05), bias and activation in fp32, one rounding at the end.
+ *   x          device, bf16 [M, K];  w: bf16 [N, K]
+ *   bias       device, float32 [N], or NULL;  residual: bf16 [M, N], or NULL
+ *   act        gelu: z Phi(z); gelu_tanh: its tanh form; silu: z / (1 + exp(-z))
+ *   out        device, out, bf16 [M, N]; may be residual itself
+ *   z          device, out, bf16 [M, N], or NULL: what sol_attn_linear_bwd needs of an activation
+ *   workspace  device, or NULL: 256 bytes, zeroed once, for sol_attn_check_device_error. Without it an
+ *              expired device wait leaves out incomplete and unreported
+ * N and K in multiples of 8, any M from 1; up to 128 rows run on a kernel of their own, whose rows
+ * may differ from the other's in the last bit. */
+sol_status sol_attn_linear(const void* x, const void* w, const float* bias, const void* residual,
+                           sol_activation act, int M, int N, int K, void* out, void* z, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace sol_attn_linear_bwd needs (0 for invalid sizes). */
+size_t sol_attn_linear_bwd_workspace_bytes(int M, int N, sol_activation act);
+
+/* Gradients of sol_attn_linear: dz = dy act'(z), dx = dz w, dw = dz^T x, db = sum of dz over rows. The
+ * gradient of residual is dy itself. dz is rounded to bf16 as an operand of dx and dw; db adds the
+ * unrounded fp32 values, in a fixed order.
+ *   dy         device, bf16 [M, N];  x, w as in the forward (NULL where only needed for a null output)
+ *   z          device, bf16 [M, N] from the forward, exactly where act is not SOL_ACT_NONE
+ *   dx         device, out, bf16 [M, K];  dw: bf16 [N, K];  db: float32 [N]; each NULL where not wanted
+ *   workspace  device, sol_attn_linear_bwd_workspace_bytes(...) bytes; only its first 256 need zeroing,
+ *              and only for sol_attn_check_device_error */
+sol_status sol_attn_linear_bwd(const void* dy, const void* x, const void* w, const void* z,
+                               sol_activation act, int M, int N, int K, void* dx, void* dw, float* db,
+                               void* workspace, size_t ws_bytes, void* stream);
+
 /* Test hook for the failure-detection path. mode 0 (default) = normal operation. mode 1 makes
  * the next sol_attn_fwd launch (SOL_BF16 path) skip one K-tile load, so the consumer's bounded
  * wait expires: the launch returns early, sets the device error word, and

@@ -125,3 +125,44 @@ def test_bindings_refuse_cpu_tensors(lib):
         sa.sol_attn_rope(q, q, torch.arange(4), torch.ones(32))
     with pytest.raises(TypeError):
         sa.sol_attn_rope_tables(torch.arange(4, dtype=torch.int32), torch.ones(32, dtype=torch.float64))
+
+
+def linear(lib, x=P[0], w=P[1], bias=P[2], res=P[3], act=1, M=4, N=64, K=64, out=P[4], z=P[5], ws=P[6], nbytes=256):
+    return lib.sol_attn_linear(x, w, bias, res, act, M, N, K, out, z, ws, nbytes, None)
+
+
+def linear_bwd(lib, dy=P[0], x=P[1], w=P[2], z=P[3], act=1, M=4, N=64, K=64, dx=P[4], dw=P[5], db=P[6], ws=P[7], nbytes=1 << 30):
+    return lib.sol_attn_linear_bwd(dy, x, w, z, act, M, N, K, dx, dw, db, ws, nbytes, None)
+
+
+def test_linear_rejects_invalid_arguments(lib):
+    for bad in (dict(x=None), dict(w=None), dict(out=None), dict(x=ODD), dict(w=ODD), dict(bias=ODD), dict(res=ODD), dict(z=ODD),
+                dict(out=ODD), dict(ws=ODD), dict(nbytes=255), dict(act=4), dict(act=-1), dict(M=0), dict(N=0), dict(K=-8)):
+        assert linear(lib, **bad) == sa.SOL_EINVAL, bad
+    for bad in (dict(N=60), dict(K=4), dict(M=1 << 28, N=1 << 28)):
+        assert linear(lib, **bad) == sa.SOL_EUNSUPPORTED, bad
+
+
+def test_linear_bwd_rejects_invalid_arguments(lib):
+    for bad in (dict(dy=None), dict(x=None), dict(w=None), dict(z=None), dict(act=0), dict(ws=None), dict(nbytes=512),
+                dict(dx=None, dw=None, db=None), dict(dy=ODD), dict(dw=ODD), dict(db=ctypes.c_void_p(0x1002)), dict(act=9),
+                dict(M=0)):
+        assert linear_bwd(lib, **bad) == sa.SOL_EINVAL, bad
+    assert linear_bwd(lib, N=4) == linear_bwd(lib, K=12) == sa.SOL_EUNSUPPORTED
+
+
+def test_linear_workspace_bytes(lib):
+    f = lib.sol_attn_linear_bwd_workspace_bytes
+    assert f(0, 8, 0) == f(8, 0, 0) == f(8, 8, 4) == 0
+    # error words, one row of partial sums at least, and dz where there is an activation
+    assert f(1, 64, 0) >= 256 + 64 * 4
+    assert f(1000, 64, 1) - f(1000, 64, 0) == 1000 * 64 * 2
+    assert f(1 << 24, 64, 0) == f(1 << 22, 64, 0) <= 1 << 20
+
+
+def test_linear_bindings_refuse_cpu_tensors(lib):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        sa.sol_attn_linear(x, x)
+    with pytest.raises(TypeError):
+        sa.sol_attn_linear_bwd(x, x, x)
