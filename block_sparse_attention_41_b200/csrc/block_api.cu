@@ -161,7 +161,7 @@ sol_status sol_attn_residual_norm(const void* x, const void* y, const float* gat
   if ((st = current_device(&sms)) != SOL_OK) return st;
   a.x_out = x_out;
   a.h = h;
-  const cudaError_t e = sol::launch_residual_norm(a, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = sol::launch_residual_norm(a, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "residual norm launch");
   return SOL_OK;
 }

@@ -132,7 +132,7 @@ struct NormArgs {
   bool bf16;
   bool vec;  // rows and vectors allow 16-byte accesses
 };
-cudaError_t launch_residual_norm(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_residual_norm(const NormArgs& a, int num_sms, cudaStream_t stream);
 
 // Its gradients. fwd.x_out, fwd.h and fwd.shift are not read.
 struct NormBwdArgs {
@@ -149,7 +149,7 @@ struct NormBwdArgs {
   float* part;         // workspace of norm_bwd_part_floats, or null where no vector's gradient is wanted
   int C, chunks;       // chunks = norm_bwd_chunks(B, T, C)
 };
-constexpr int kNormBwdBlocks = 592;  // blocks over all batch entries: 4 per SM
+constexpr int kNormBwdBlocks = 592;  // 4 per SM, of which 1 to 3 are taken over all batch entries
 int norm_bwd_chunks(int B, int T, int C);
 size_t norm_bwd_part_floats(int B, int T, int C);
 cudaError_t launch_residual_norm_bwd(const NormBwdArgs& a, cudaStream_t stream);

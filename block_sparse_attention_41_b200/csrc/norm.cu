@@ -6,11 +6,15 @@
 // C channels of a row. Every vector (gate, gains, scale, shift) may be absent.
 //
 // HBM-bound: x and y are read once, x' and h written once; a row stays in registers between. A
-// thread owns the same 16 (backward: 8) channels of every row, in 16-byte vectors (or single values where C
-// or an address does not allow those); rows are reduced by warp shuffles and, where a row spans
-// several warps, one shared-memory exchange per statistic. Variance is taken about the mean in a
-// second reduction over the registers, not as a difference of moments, so a large common offset
-// costs no digits. All arithmetic is fp32; only the stored rows are rounded.
+// thread owns the same E channels of every row of its batch entry, in 16-byte vectors, with the
+// vectors' products (gate post_gain and gain (1 + scale)) formed once, and keeps the next rows on
+// their way with asynchronous copies into a ring in shared memory that belongs to the thread alone:
+// no barrier and no wait on another thread, and enough bytes in flight while rows are reduced. Rows
+// whose length or address does not allow 16-byte accesses are read value by value. Rows are reduced
+// by warp shuffles and, where a row spans several warps, one shared-memory exchange per statistic.
+// Variance is taken about the mean in a second reduction over the registers, not as a difference of
+// moments, so a large common offset costs no digits. All arithmetic is fp32, two channels per
+// instruction; only the stored rows are rounded.
 #include <cmath>
 
 #include "device_common.cuh"
@@ -20,229 +24,409 @@ namespace sol {
 
 namespace {
 
-constexpr int kFwdElems = 16;  // channels per thread
-constexpr int kBwdElems = 8;   // fewer than forward: the sums of three gradients stay in registers too
-constexpr int kMaxWarps = 32;
+constexpr int kMaxWarps = 16;  // of a row
+constexpr int kMaxRows = 16;   // of several warps in a block: 15 named barriers
+constexpr int kSmemMax = 227 * 1024;  // per block
 
-// ---- element access: V consecutive values as fp32 ------------------------------------------------
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[V]) {
+// ---- two fp32 values per register pair ---------------------------------------------------------------
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(f2 v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+  const float2 t = unpack2(v);
+  return t.x + t.y;
+}
+
+// ---- element access ------------------------------------------------------------------------------------
+// A 16-byte vector (V = 8 bf16 or 4 fp32) as V / 2 pairs, and back.
+template <int V>
+__device__ __forceinline__ void widen(const uint4& v, f2* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   if constexpr (V == 8) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) x[k] = pack2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+  }
+}
+template <int V>
+__device__ __forceinline__ uint4 narrow(const f2* x) {
+  uint32_t w[4];
+  if constexpr (V == 8) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(w[k] << 16);
-      x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      const float2 t = unpack2(x[k]);
+      w[k] = pack_bf16x2(t.x, t.y);
     }
-  } else if constexpr (V == 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else if constexpr (sizeof(T) == 2) {
-    x[0] = __bfloat162float(*p);
-  } else {
-    x[0] = __ldg(p);
-  }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
-  if constexpr (V == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  } else if constexpr (sizeof(T) == 2) {
-    *p = __float2bfloat16_rn(x[0]);
-  } else {
-    *p = x[0];
-  }
-}
-// V values of an fp32 vector (16-byte aligned where V > 1)
-template <int V>
-__device__ __forceinline__ void load_param(const float* p, float (&x)[V]) {
-  if constexpr (V == 1) {
-    x[0] = __ldg(p);
   } else {
 #pragma unroll
-    for (int k = 0; k < V; k += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p + k));
-      x[k] = v.x; x[k + 1] = v.y; x[k + 2] = v.z; x[k + 3] = v.w;
+    for (int k = 0; k < 2; ++k) {
+      const float2 t = unpack2(x[k]);
+      w[2 * k] = __float_as_uint(t.x);
+      w[2 * k + 1] = __float_as_uint(t.y);
     }
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One row spread over `tpr` consecutive threads (a multiple of 32) of a block that holds blockDim.x
-// / tpr rows. The exchange buffer alternates between its two halves, so one barrier per reduction
-// is enough: a half is written again only behind the barrier of the reduction in between.
-struct RowGroup {
-  float* buf;  // [2][kMaxWarps][2]
-  int first_warp, nwarps, warp, lane, phase;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The E channels of a row that a thread owns, E / V vectors of V consecutive ones (V = 8 or 4: 16
+// bytes; V = 1: single values), and its part of shared memory: 16-byte slots, one per thread side by
+// side. FULL: every vector lies within the row, and a row has whole warps. Rows are addressed by the byte offset of the thread's
+// first channel, which the loops carry along: forming it anew costs more than the arithmetic.
+template <typename T, int V, int E, bool FULL>
+struct Lane {
+  static constexpr int NV = E / V, P = E / 2;
+  int tpr, t, C;
+  uint32_t smem, step;
+
+  __device__ __forceinline__ int chan(int j) const { return (j * tpr + t) * V; }
+  __device__ __forceinline__ bool on(int j) const { return FULL || chan(j) < C; }
+  __device__ __forceinline__ uint32_t slot(int i) const { return smem + static_cast<uint32_t>(i) * step; }
+  __device__ __forceinline__ const T* at(const void* base, size_t o, int j) const {
+    return reinterpret_cast<const T*>(static_cast<const char*>(base) + o + j * tpr * V * static_cast<int>(sizeof(T)));
+  }
+  __device__ __forceinline__ T* at(void* base, size_t o, int j) const {
+    return reinterpret_cast<T*>(static_cast<char*>(base) + o + j * tpr * V * static_cast<int>(sizeof(T)));
+  }
+
+  // a row from global memory
+  __device__ __forceinline__ void load(const void* base, size_t o, f2 (&x)[P]) const {
+    if constexpr (V > 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (on(j)) widen<V>(__ldg(reinterpret_cast<const uint4*>(at(base, o, j))), &x[j * V / 2]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        x[i] = pack2(on(2 * i) ? static_cast<float>(*at(base, o, 2 * i)) : 0.f,
+                     on(2 * i + 1) ? static_cast<float>(*at(base, o, 2 * i + 1)) : 0.f);
+    }
+  }
+  __device__ __forceinline__ void store(void* base, size_t o, const f2 (&x)[P]) const {
+    if constexpr (V > 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (on(j)) *reinterpret_cast<uint4*>(at(base, o, j)) = narrow<V>(&x[j * V / 2]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 v = unpack2(x[i]);
+        if (on(2 * i)) put(at(base, o, 2 * i), v.x);
+        if (on(2 * i + 1)) put(at(base, o, 2 * i + 1), v.y);
+      }
+    }
+  }
+  static __device__ __forceinline__ void put(T* p, float v) {
+    if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(v);
+    else *p = v;
+  }
+  // a row on its way to the slots from i on, and out of slots at an address
+  __device__ __forceinline__ void fetch(const void* base, size_t o, uint32_t to) const {
+    if constexpr (V > 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (on(j)) cp_async16(to + j * step, at(base, o, j));
+    }
+  }
+  __device__ __forceinline__ void take(uint32_t from, f2 (&x)[P]) const {
+    if constexpr (V > 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (on(j)) widen<V>(lds128(from + j * step), &x[j * V / 2]);
+    }
+  }
+  // an fp32 vector (16-byte aligned where V > 1); channels past C and an absent vector read as `absent`
+  __device__ __forceinline__ void param(const float* p, float absent, f2 (&x)[P]) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = pack2(absent, absent);
+    if (p == nullptr) return;
+    if constexpr (V > 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!on(j)) continue;
+#pragma unroll
+        for (int k = 0; k < V; k += 4) widen<4>(__ldg(reinterpret_cast<const uint4*>(p + chan(j) + k)), &x[(j * V + k) / 2]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        x[i] = pack2(on(2 * i) ? __ldg(p + chan(2 * i)) : absent, on(2 * i + 1) ? __ldg(p + chan(2 * i + 1)) : absent);
+    }
+  }
+  // zeros in the channels past C
+  __device__ __forceinline__ void mask(f2 (&x)[P]) const {
+    if constexpr (!FULL) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 v = unpack2(x[i]);
+        x[i] = pack2(on(2 * i / V) ? v.x : 0.f, on((2 * i + 1) / V) ? v.y : 0.f);
+      }
+    }
+  }
 };
 
-// Sums of N values over a row. Every thread of the block calls it the same number of times.
+// One row spread over `tpr` consecutive threads, a power of two up to 32 or a multiple of 32, of a
+// block that holds blockDim.x / tpr rows. The exchange buffer alternates between its two halves, so
+// one barrier per reduction is enough: a half is written again only behind the barrier of the
+// reduction in between. Each row of a block has a barrier of its own.
+struct RowGroup {
+  float* buf;  // the row's [2][2][kMaxWarps]: half, value, warp (zero past nwarps)
+  int nwarps, width, lane, warp, phase, sub, tpr;
+};
+
+// s_buf: [kMaxRows][2][2][kMaxWarps], zeroed here; the caller meets at a barrier before the first sum.
+__device__ __forceinline__ RowGroup row_group(float* s_buf, int tpr) {
+  RowGroup g;
+  g.lane = threadIdx.x & 31;
+  g.nwarps = tpr > 32 ? tpr >> 5 : 1;
+  g.width = tpr > 32 ? 32 : tpr;
+  g.sub = threadIdx.x / tpr;
+  g.warp = (threadIdx.x >> 5) - (tpr > 32 ? g.sub * g.nwarps : 0);  // within the row, where it has several
+  g.buf = s_buf + (tpr > 32 ? g.sub : 0) * 4 * kMaxWarps;
+  g.phase = 0;
+  g.tpr = tpr;
+  for (int i = threadIdx.x; i < kMaxRows * 4 * kMaxWarps; i += blockDim.x) s_buf[i] = 0.f;
+  return g;
+}
+
+// Sums of N values over a row, the same for all its threads. Each thread adds the warps' sums itself:
+// a few 16-byte broadcasts take a third of the latency of five more shuffles.
 template <int N>
 __device__ __forceinline__ void row_sum(RowGroup& g, float (&v)[N]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
+    if (o < g.width) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
   }
   if (g.nwarps == 1) return;
-  float* b = g.buf + g.phase * (kMaxWarps * 2);
+  float* b = g.buf + g.phase * (2 * kMaxWarps);
   g.phase ^= 1;
   if (g.lane == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) b[g.warp * 2 + i] = v[i];
+    for (int i = 0; i < N; ++i) b[i * kMaxWarps + g.warp] = v[i];
   }
-  __syncthreads();
+  named_barrier_sync(1 + g.sub, g.tpr);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float s = g.lane < g.nwarps ? b[(g.first_warp + g.lane) * 2 + i] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float4* q = reinterpret_cast<const float4*>(b + i * kMaxWarps);
+    const float4 a = q[0], c = q[1];
+    float s = ((a.x + a.y) + (a.z + a.w)) + ((c.x + c.y) + (c.z + c.w));
+    if (g.nwarps > 8) {
+      const float4 d = q[2], e = q[3];
+      s += ((d.x + d.y) + (d.z + d.w)) + ((e.x + e.y) + (e.z + e.w));
+    }
     v[i] = s;
   }
 }
 
-// The row's values, normalised in place; returns 1 / sqrt(mean square or variance + eps). Channels
-// past C (on[j] false) hold zeros before and after.
-template <int V, int NV>
-__device__ __forceinline__ float normalise(RowGroup& g, float (&x)[NV][V], const bool (&on)[NV], int kind, float inv_c,
-                                           float eps) {
+// The row's values, centred for a layer norm; returns 1 / sqrt(mean square + eps), by which they are
+// still to be multiplied. Channels past C hold zeros before and after.
+template <typename L>
+__device__ __forceinline__ float centre(const L& l, RowGroup& g, f2 (&x)[L::P], int kind, float inv_c, float eps) {
   if (kind == NORM_LAYER) {
-    float s[1] = {0.f};
+    f2 s = x[0];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int i = 1; i < L::P; ++i) s = add2(s, x[i]);
+    float v[1] = {sum2(s)};
+    row_sum(g, v);
+    const f2 m = pack2(-v[0] * inv_c, -v[0] * inv_c);
 #pragma unroll
-      for (int k = 0; k < V; ++k) s[0] += x[j][k];
-    row_sum(g, s);
-    const float mean = s[0] * inv_c;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < V; ++k) x[j][k] = on[j] ? x[j][k] - mean : 0.f;
+    for (int i = 0; i < L::P; ++i) x[i] = add2(x[i], m);
+    l.mask(x);
   }
-  float q[1] = {0.f};
+  f2 q = mul2(x[0], x[0]);
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int i = 1; i < L::P; ++i) q = fma2(x[i], x[i], q);
+  float v[1] = {sum2(q)};
+  row_sum(g, v);
+  return 1.0f / sqrtf(fmaf(v[0], inv_c, eps));
+}
+template <int P>
+__device__ __forceinline__ void scale_by(f2 (&x)[P], float r) {
+  const f2 rr = pack2(r, r);
 #pragma unroll
-    for (int k = 0; k < V; ++k) q[0] = fmaf(x[j][k], x[j][k], q[0]);
-  row_sum(g, q);
-  const float r = 1.0f / sqrtf(fmaf(q[0], inv_c, eps));
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int k = 0; k < V; ++k) x[j][k] *= r;
-  return r;
+  for (int i = 0; i < P; ++i) x[i] = mul2(x[i], rr);
 }
 
-// Gradient of a row from the gradient w of its normalised values n: r (w - [mean w] - n mean(w n)),
-// in place in w.
-template <int V, int NV>
-__device__ __forceinline__ void normalise_back(RowGroup& g, float (&w)[NV][V], const float (&n)[NV][V], float r,
-                                               int kind, float inv_c) {
-  float s[2] = {0.f, 0.f};
+// Gradient of a row from the gradient w of its normalised values n, added to `to`:
+// to + r (w - [mean w] - n mean(w n)). Channels past C hold zeros before and after.
+template <typename L>
+__device__ __forceinline__ void normalise_back(const L& l, RowGroup& g, f2 (&w)[L::P], const f2 (&n)[L::P], float r, int kind,
+                                               float inv_c) {
+  f2 s = mul2(w[0], n[0]);
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int i = 1; i < L::P; ++i) s = fma2(w[i], n[i], s);
+  f2 m = pack2(0.f, 0.f);
+  float a;
+  if (kind == NORM_LAYER) {
+    m = w[0];
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      s[0] = fmaf(w[j][k], n[j][k], s[0]);
-      s[1] += w[j][k];
-    }
-  row_sum(g, s);
-  const float a = s[0] * inv_c, m = kind == NORM_LAYER ? s[1] * inv_c : 0.f;
+    for (int i = 1; i < L::P; ++i) m = add2(m, w[i]);
+    float v[2] = {sum2(s), sum2(m)};
+    row_sum(g, v);
+    a = -v[0] * inv_c * r;
+    m = pack2(-v[1] * inv_c, -v[1] * inv_c);
+  } else {
+    float v[1] = {sum2(s)};
+    row_sum(g, v);
+    a = -v[0] * inv_c * r;
+  }
+  const f2 rr = pack2(r, r), aa = pack2(a, a);
+  // w - mean before the multiplication by r: a large common part of w leaves without rounding with it
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int k = 0; k < V; ++k) w[j][k] = r * (w[j][k] - m - n[j][k] * a);
-}
-
-__device__ __forceinline__ RowGroup row_group(float* buf, int tpr) {
-  RowGroup g;
-  g.buf = buf;
-  g.warp = threadIdx.x >> 5;
-  g.lane = threadIdx.x & 31;
-  g.nwarps = tpr >> 5;
-  g.first_warp = g.warp / g.nwarps * g.nwarps;
-  g.phase = 0;
-  return g;
+  for (int i = 0; i < L::P; ++i) w[i] = fma2(n[i], aa, mul2(kind == NORM_LAYER ? add2(w[i], m) : w[i], rr));
+  l.mask(w);
 }
 
 // ---- forward ---------------------------------------------------------------------------------------
-template <typename T, int V, int E, int MAXT>
-__global__ void __launch_bounds__(MAXT) sol_residual_norm_kernel(const __grid_constant__ NormArgs p, int tpr) {
-  constexpr int NV = E / V;
-  __shared__ float s_buf[2 * kMaxWarps * 2];
+// A block's groups of tpr threads take rows of one batch entry, so they share the vectors' products in
+// shared memory: A = gate post_gain, S = gain (1 + scale), H = shift. (In registers they left room
+// for half as many threads and spilled: 874 us at 75600 x 5120 bf16; read per row from L1, 793 us.)
+// RING: the next row is on its way while one is reduced; else direct loads.
+template <typename T, int V, int E, bool RING, bool FULL, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid_constant__ NormArgs p, int tpr, int chunks) {
+  using L = Lane<T, V, E, FULL>;
+  constexpr int kParam = E / 4;  // slots of a product
+  extern __shared__ uint4 s_mem[];  // products [3][kParam][tpr], ring [R][tensors][NV][threads]
+  __shared__ float s_buf[kMaxRows * 4 * kMaxWarps];
   RowGroup g = row_group(s_buf, tpr);
-  const int rpb = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
-  const long long rows = static_cast<long long>(p.B) * p.T;
+  const int rpb = blockDim.x / tpr, t = threadIdx.x - g.sub * tpr;
+  const uint32_t ring = smem_u32(s_mem) + 3 * kParam * tpr * 16 + threadIdx.x * 16;
+  const L l{tpr, t, p.C, ring, blockDim.x * 16u};
+  const int b = blockIdx.x / chunks, chunk = blockIdx.x - b * chunks;
   const float inv_c = 1.0f / static_cast<float>(p.C);
-  bool on[NV];
-  int c[NV];
+  const bool has_y = p.y != nullptr;
+  const uint32_t slot_bytes = (has_y ? 2 : 1) * L::NV * l.step;
+  const int stride = chunks * rpb;  // a block's last rows may be past the end
+  const size_t step = static_cast<size_t>(stride) * p.C * sizeof(T);
+  int row = chunk * rpb + g.sub;
+  size_t o = (static_cast<size_t>(b) * p.T + row) * p.C * sizeof(T) + static_cast<size_t>(l.chan(0)) * sizeof(T);
+  auto fetch = [&](int r, size_t from, uint32_t to) {
+    if (r < p.T) {
+      l.fetch(p.x, from, to);
+      if (has_y) l.fetch(p.y, from, to + L::NV * l.step);
+    }
+    cp_async_commit();
+  };
+  if constexpr (RING) fetch(row, o, ring);
+  const uint32_t prod = smem_u32(s_mem) + t * 16;
+  if (g.sub == 0) {
+    f2 u[L::P], v[L::P];
+    auto put = [&](int at) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    c[j] = (j * tpr + t) * V;
-    on[j] = c[j] < p.C;
+      for (int i = 0; i < kParam; ++i) sts128(prod + (at * kParam + i) * tpr * 16, narrow<4>(&v[2 * i]));
+    };
+    l.param(p.gate != nullptr ? p.gate + b * p.gate_stride : nullptr, 1.f, v);
+    l.param(p.post_gain, 1.f, u);
+#pragma unroll
+    for (int i = 0; i < L::P; ++i) v[i] = mul2(v[i], u[i]);
+    put(0);
+    l.param(p.scale != nullptr ? p.scale + b * p.scale_stride : nullptr, 0.f, v);
+    l.param(p.gain, 1.f, u);
+#pragma unroll
+    for (int i = 0; i < L::P; ++i) v[i] = fma2(v[i], u[i], u[i]);
+    put(1);
+    l.param(p.shift != nullptr ? p.shift + b * p.shift_stride : nullptr, 0.f, v);
+    put(2);
   }
-  for (long long r0 = static_cast<long long>(blockIdx.x) * rpb; r0 < rows; r0 += static_cast<long long>(gridDim.x) * rpb) {
-    const long long row = r0 + sub;
-    const bool live = row < rows;  // a block's last rows may be past the end; their threads still meet at the barriers
-    const size_t base = live ? static_cast<size_t>(row) * p.C : 0;
-    const int b = live ? static_cast<int>(row / p.T) : 0;
-    float x[NV][V], y[NV][V];
+  __syncthreads();
+  auto product = [&](int at, int i, f2 (&m)[2]) { widen<4>(lds128(prod + (at * kParam + i) * tpr * 16), m); };
+  const f2 res = pack2(p.res_scale, p.res_scale);
+  uint32_t now = ring, next = ring + slot_bytes;
+  // a row of several warps stops by itself; rows that share a warp stop with the block's first
+  for (int lead = FULL ? row : chunk * rpb; lead < p.T; lead += stride, row += stride, o += step) {
+    const bool go = FULL || row < p.T;
+    f2 x[L::P], y[L::P];
+    if constexpr (!FULL) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+      for (int k = 0; k < L::P; ++k) x[k] = y[k] = pack2(0.f, 0.f);
+    }
+    if constexpr (RING) {
+      fetch(row + stride, o + step, next);
+      cp_async_wait<1>();
+    }
+    if (has_y) {
+      if (go) {
+        if constexpr (RING) l.take(now + L::NV * l.step, y);
+        else l.load(p.y, o, y);
+      }
+      if (p.post_norm != NORM_NONE) scale_by(y, centre(l, g, y, p.post_norm, inv_c, p.eps));
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[j][k] = y[j][k] = 0.f;
-      if (live && on[j]) {
-        load_vec<T, V>(static_cast<const T*>(p.x) + base + c[j], x[j]);
-        if (p.y != nullptr) load_vec<T, V>(static_cast<const T*>(p.y) + base + c[j], y[j]);
+      for (int i = 0; i < kParam; ++i) {
+        f2 m[2];
+        product(0, i, m);
+        y[2 * i] = mul2(y[2 * i], m[0]);
+        y[2 * i + 1] = mul2(y[2 * i + 1], m[1]);
       }
     }
-    if (p.y != nullptr) {
-      if (p.post_norm != NORM_NONE) normalise<V, NV>(g, y, on, p.post_norm, inv_c, p.eps);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (!on[j]) continue;
-        float w[V];
-        if (p.post_gain != nullptr) {
-          load_param<V>(p.post_gain + c[j], w);
-#pragma unroll
-          for (int k = 0; k < V; ++k) y[j][k] *= w[k];
-        }
-        if (p.gate != nullptr) {
-          load_param<V>(p.gate + static_cast<size_t>(b) * p.gate_stride + c[j], w);
-#pragma unroll
-          for (int k = 0; k < V; ++k) y[j][k] *= w[k];
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) x[j][k] = fmaf(p.res_scale, x[j][k], y[j][k]);
-        if (live) store_vec<T, V>(static_cast<T*>(p.x_out) + base + c[j], x[j]);
-      }
+    if (go) {
+      if constexpr (RING) l.take(now, x);
+      else l.load(p.x, o, x);
     }
-    normalise<V, NV>(g, x, on, p.norm, inv_c, p.eps);
+    if (has_y) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!on[j] || !live) continue;
-      float w[V];
-      if (p.gain != nullptr) {
-        load_param<V>(p.gain + c[j], w);
-#pragma unroll
-        for (int k = 0; k < V; ++k) x[j][k] *= w[k];
-      }
-      if (p.scale != nullptr) {
-        load_param<V>(p.scale + static_cast<size_t>(b) * p.scale_stride + c[j], w);
-#pragma unroll
-        for (int k = 0; k < V; ++k) x[j][k] = fmaf(x[j][k], w[k], x[j][k]);
-      }
-      if (p.shift != nullptr) {
-        load_param<V>(p.shift + static_cast<size_t>(b) * p.shift_stride + c[j], w);
-#pragma unroll
-        for (int k = 0; k < V; ++k) x[j][k] += w[k];
-      }
-      store_vec<T, V>(static_cast<T*>(p.h) + base + c[j], x[j]);
+      for (int k = 0; k < L::P; ++k) x[k] = fma2(res, x[k], y[k]);
+      if (go) l.store(p.x_out, o, x);
     }
+    const float r = centre(l, g, x, p.norm, inv_c, p.eps);
+    const f2 rr = pack2(r, r);
+#pragma unroll
+    for (int i = 0; i < kParam; ++i) {
+      f2 m[2], h[2];
+      product(1, i, m);
+      product(2, i, h);
+      x[2 * i] = fma2(mul2(x[2 * i], rr), m[0], h[0]);
+      x[2 * i + 1] = fma2(mul2(x[2 * i + 1], rr), m[1], h[1]);
+    }
+    if (go) l.store(p.h, o, x);
+    const uint32_t free = now;
+    now = next;
+    next = free;
   }
+  if constexpr (RING) cp_async_wait<0>();
 }
 
 // ---- backward --------------------------------------------------------------------------------------
@@ -252,134 +436,172 @@ __global__ void __launch_bounds__(MAXT) sol_residual_norm_kernel(const __grid_co
 // and over the rows of a batch entry, per channel: P = sum dh n, S = sum dh, Q = sum D ny. From them
 //   dscale = gain P, dshift = S, dgate = post_gain Q, dgain = sum_b (1 + scale) P, dpost_gain = sum_b gate Q.
 // x' and its statistics are formed again from x and y, so the forward pass keeps nothing. P, S and
-// Q stay in registers over a block's rows, go to the workspace once per block, and a second kernel
-// adds the blocks in a fixed order: no atomics, the same bits every time.
-template <typename T, int V, int E, int MAXT>
-__global__ void __launch_bounds__(MAXT) sol_residual_norm_bwd_kernel(const __grid_constant__ NormBwdArgs p, int tpr) {
-  constexpr int NV = E / V;
-  __shared__ float s_buf[2 * kMaxWarps * 2];
+// Q stay in registers over a block's rows, are added over the rows that a block holds side by side,
+// go to the workspace once per block, and a second kernel adds the blocks in a fixed order: no
+// atomics, the same bits every time. With three sums, n, ny and w in registers the vectors' products
+// have no room there; they lie in the thread's slots of shared memory.
+template <typename T, int V, int E, bool RING, bool FULL, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const __grid_constant__ NormBwdArgs p, int tpr) {
+  using L = Lane<T, V, E, FULL>;
+  extern __shared__ uint4 s_ring[];
+  __shared__ float s_buf[kMaxRows * 4 * kMaxWarps];
   RowGroup g = row_group(s_buf, tpr);
-  const int rpb = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
+  const NormArgs& f = p.fwd;
+  const int rpb = blockDim.x / tpr;
   const int b = blockIdx.x / p.chunks, chunk = blockIdx.x - b * p.chunks;
   const float inv_c = 1.0f / static_cast<float>(p.C);
-  const NormArgs& f = p.fwd;
-  bool on[NV];
-  int c[NV];
-  float aP[NV][V], aS[NV][V], aQ[NV][V];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    c[j] = (j * tpr + t) * V;
-    on[j] = c[j] < p.C;
-#pragma unroll
-    for (int k = 0; k < V; ++k) aP[j][k] = aS[j][k] = aQ[j][k] = 0.f;
-  }
-  for (int r0 = chunk * rpb; r0 < f.T; r0 += p.chunks * rpb) {
-    const int row = r0 + sub;
-    const bool live = row < f.T;
-    const size_t base = (static_cast<size_t>(b) * f.T + (live ? row : 0)) * p.C;
-    float x[NV][V], y[NV][V], w[NV][V], d[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) x[j][k] = y[j][k] = w[j][k] = d[j][k] = 0.f;
-      if (live && on[j]) {
-        load_vec<T, V>(static_cast<const T*>(f.x) + base + c[j], x[j]);
-        if (f.y != nullptr) load_vec<T, V>(static_cast<const T*>(f.y) + base + c[j], y[j]);
-        load_vec<T, V>(static_cast<const T*>(p.dh) + base + c[j], w[j]);
-        if (p.dx_out != nullptr) load_vec<T, V>(static_cast<const T*>(p.dx_out) + base + c[j], d[j]);
-      }
+  const bool has_y = f.y != nullptr, has_d = p.dx_out != nullptr;
+  // slots: gain (1 + scale), gate post_gain, then the ring: x, dh, and y and dx_out where they are
+  constexpr int kParam = E / 4;
+  const int tensors = 2 + has_y + has_d;
+  const L l{tpr, static_cast<int>(threadIdx.x) - g.sub * tpr, p.C, smem_u32(s_ring) + threadIdx.x * 16u, blockDim.x * 16u};
+  const uint32_t ring = l.slot(2 * kParam), slot_bytes = tensors * L::NV * l.step;
+  const int stride = p.chunks * rpb;
+  const size_t step = static_cast<size_t>(stride) * p.C * sizeof(T);
+  int row = chunk * rpb + g.sub;
+  size_t o = (static_cast<size_t>(b) * f.T + row) * p.C * sizeof(T) + static_cast<size_t>(l.chan(0)) * sizeof(T);
+  auto fetch = [&](int r, size_t from, uint32_t to) {
+    if (r < f.T) {
+      l.fetch(f.x, from, to);
+      l.fetch(p.dh, from, to + L::NV * l.step);
+      if (has_y) l.fetch(f.y, from, to + 2 * L::NV * l.step);
+      if (has_d) l.fetch(p.dx_out, from, to + 3 * L::NV * l.step);  // only with y
     }
+    cp_async_commit();
+  };
+  if constexpr (RING) fetch(row, o, ring);
+  f2 aP[L::P], aS[L::P], aQ[L::P];
+  {
+    f2 u[L::P], v[L::P];
+    l.param(f.scale != nullptr ? f.scale + static_cast<size_t>(b) * f.scale_stride : nullptr, 0.f, v);
+    l.param(f.gain, 1.f, u);
+#pragma unroll
+    for (int i = 0; i < L::P; ++i) v[i] = fma2(v[i], u[i], u[i]);
+#pragma unroll
+    for (int i = 0; i < kParam; ++i) sts128(l.slot(i), narrow<4>(&v[2 * i]));
+    l.param(f.gate != nullptr ? f.gate + static_cast<size_t>(b) * f.gate_stride : nullptr, 1.f, v);
+    l.param(f.post_gain, 1.f, u);
+#pragma unroll
+    for (int i = 0; i < L::P; ++i) v[i] = mul2(v[i], u[i]);
+#pragma unroll
+    for (int i = 0; i < kParam; ++i) sts128(l.slot(kParam + i), narrow<4>(&v[2 * i]));
+  }
+#pragma unroll
+  for (int i = 0; i < L::P; ++i) aP[i] = aS[i] = aQ[i] = pack2(0.f, 0.f);
+  // v times the vector in the slots from `at` on
+  auto times = [&](const f2 (&v)[L::P], int at, f2 (&out)[L::P]) {
+#pragma unroll
+    for (int i = 0; i < kParam; ++i) {
+      f2 m[2];
+      widen<4>(lds128(l.slot(at + i)), m);
+      out[2 * i] = mul2(v[2 * i], m[0]);
+      out[2 * i + 1] = mul2(v[2 * i + 1], m[1]);
+    }
+  };
+  const f2 res = pack2(f.res_scale, f.res_scale);
+  __syncthreads();  // the exchange buffer is zeroed
+  uint32_t now = ring, next = ring + slot_bytes;
+  for (int lead = FULL ? row : chunk * rpb; lead < f.T; lead += stride, row += stride, o += step) {
+    const bool live = FULL || row < f.T;
+    f2 x[L::P], y[L::P], w[L::P];
+    if constexpr (!FULL) {
+#pragma unroll
+      for (int k = 0; k < L::P; ++k) x[k] = y[k] = w[k] = pack2(0.f, 0.f);
+    }
+    if constexpr (RING) {
+      fetch(row + stride, o + step, next);
+      cp_async_wait<1>();
+    }
+    auto read = [&](int tensor, const void* from, f2 (&v)[L::P]) {
+      if constexpr (RING) l.take(now + tensor * L::NV * l.step, v);
+      else l.load(from, o, v);
+    };
+    if (live) read(0, f.x, x);
     float ry = 0.f;
-    if (f.y != nullptr) {
-      if (f.post_norm != NORM_NONE) ry = normalise<V, NV>(g, y, on, f.post_norm, inv_c, f.eps);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (!on[j]) continue;
-        float u[V], v[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) u[k] = y[j][k];
-        if (f.post_gain != nullptr) {
-          load_param<V>(f.post_gain + c[j], v);
-#pragma unroll
-          for (int k = 0; k < V; ++k) u[k] *= v[k];
-        }
-        if (f.gate != nullptr) {
-          load_param<V>(f.gate + static_cast<size_t>(b) * f.gate_stride + c[j], v);
-#pragma unroll
-          for (int k = 0; k < V; ++k) u[k] *= v[k];
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) x[j][k] = fmaf(f.res_scale, x[j][k], u[k]);
+    if (has_y) {
+      if (live) read(2, f.y, y);
+      if (f.post_norm != NORM_NONE) {
+        ry = centre(l, g, y, f.post_norm, inv_c, f.eps);
+        scale_by(y, ry);
       }
+      times(y, kParam, w);
+#pragma unroll
+      for (int k = 0; k < L::P; ++k) x[k] = fma2(res, x[k], w[k]);
     }
-    const float r = normalise<V, NV>(g, x, on, f.norm, inv_c, f.eps);
+    const float r = centre(l, g, x, f.norm, inv_c, f.eps);
+    scale_by(x, r);
+    if constexpr (!FULL) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!on[j]) continue;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        aP[j][k] = fmaf(w[j][k], x[j][k], aP[j][k]);
-        aS[j][k] += w[j][k];
-      }
-      float v[V];
-      if (f.gain != nullptr) {
-        load_param<V>(f.gain + c[j], v);
-#pragma unroll
-        for (int k = 0; k < V; ++k) w[j][k] *= v[k];
-      }
-      if (f.scale != nullptr) {
-        load_param<V>(f.scale + static_cast<size_t>(b) * f.scale_stride + c[j], v);
-#pragma unroll
-        for (int k = 0; k < V; ++k) w[j][k] = fmaf(w[j][k], v[k], w[j][k]);
-      }
+      for (int k = 0; k < L::P; ++k) w[k] = pack2(0.f, 0.f);
     }
-    normalise_back<V, NV>(g, w, x, r, f.norm, inv_c);
+    if (live) read(1, p.dh, w);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!on[j]) continue;
-      float o[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        d[j][k] += w[j][k];
-        o[k] = f.y != nullptr ? f.res_scale * d[j][k] : d[j][k];
-      }
-      if (live) store_vec<T, V>(static_cast<T*>(p.dx) + base + c[j], o);
+    for (int k = 0; k < L::P; ++k) {
+      aP[k] = fma2(w[k], x[k], aP[k]);
+      aS[k] = add2(aS[k], w[k]);
     }
-    if (f.y != nullptr) {
+    times(w, 0, w);
+    normalise_back(l, g, w, x, r, f.norm, inv_c);
+    if (has_d && live) {
+      f2 d[L::P];
+      if constexpr (!FULL) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (!on[j]) continue;
-        float v[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) aQ[j][k] = fmaf(d[j][k], y[j][k], aQ[j][k]);
-        if (f.gate != nullptr) {
-          load_param<V>(f.gate + static_cast<size_t>(b) * f.gate_stride + c[j], v);
-#pragma unroll
-          for (int k = 0; k < V; ++k) d[j][k] *= v[k];
-        }
-        if (f.post_gain != nullptr) {
-          load_param<V>(f.post_gain + c[j], v);
-#pragma unroll
-          for (int k = 0; k < V; ++k) d[j][k] *= v[k];
-        }
+        for (int k = 0; k < L::P; ++k) d[k] = pack2(0.f, 0.f);
       }
-      if (f.post_norm != NORM_NONE) normalise_back<V, NV>(g, d, y, ry, f.post_norm, inv_c);
+      read(3, p.dx_out, d);
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (live && on[j]) store_vec<T, V>(static_cast<T*>(p.dy) + base + c[j], d[j]);
+      for (int k = 0; k < L::P; ++k) w[k] = add2(w[k], d[k]);
+    }
+    if (has_y) {
+#pragma unroll
+      for (int k = 0; k < L::P; ++k) x[k] = mul2(w[k], res);
+      if (live) l.store(p.dx, o, x);
+#pragma unroll
+      for (int k = 0; k < L::P; ++k) aQ[k] = fma2(w[k], y[k], aQ[k]);
+      times(w, kParam, w);
+      if (f.post_norm != NORM_NONE) normalise_back(l, g, w, y, ry, f.post_norm, inv_c);
+      if (live) l.store(p.dy, o, w);
+    } else if (live) {
+      l.store(p.dx, o, w);
+    }
+    const uint32_t free = now;
+    now = next;
+    next = free;
+  }
+  if constexpr (RING) cp_async_wait<0>();
+  if (p.part == nullptr) return;
+  // a row past the end added zeros only; rows side by side: first those of a warp, then warp by warp
+  for (int q = tpr; q < 32; q <<= 1) {
+#pragma unroll
+    for (int i = 0; i < L::P; ++i) {
+      aP[i] = add2(aP[i], __shfl_xor_sync(0xffffffffu, aP[i], q));
+      aS[i] = add2(aS[i], __shfl_xor_sync(0xffffffffu, aS[i], q));
+      aQ[i] = add2(aQ[i], __shfl_xor_sync(0xffffffffu, aQ[i], q));
     }
   }
-  // a row past the end added zeros only
-  if (p.part != nullptr) {
-    float* part = p.part + static_cast<size_t>(blockIdx.x * rpb + sub) * 3 * p.C;
+  const int held = tpr < 32 ? blockDim.x / 32 : rpb, mine = tpr < 32 ? g.warp : g.sub;  // sums to add
+  const bool writer = tpr >= 32 || g.lane < tpr;
+  float* s_sum = reinterpret_cast<float*>(s_ring);  // [3][C], over the slots
+  float* part = p.part + static_cast<size_t>(blockIdx.x) * 3 * p.C;
+  for (int s = 0; s < held; ++s) {
+    if (held > 1) __syncthreads();
+    if (s != mine || !writer) continue;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!on[j]) continue;
+    for (int i = 0; i < L::P; ++i) {
+      const f2 sums[3] = {aP[i], aS[i], aQ[i]};
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        part[c[j] + k] = aP[j][k];
-        part[p.C + c[j] + k] = aS[j][k];
-        if (f.y != nullptr) part[2 * static_cast<size_t>(p.C) + c[j] + k] = aQ[j][k];
+      for (int k = 0; k < 2; ++k) {
+        const int e = 2 * i + k;
+        if (!l.on(e / V)) continue;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          const float2 pair = unpack2(sums[q]);
+          float v = k == 0 ? pair.x : pair.y;
+          const int to = q * p.C + l.chan(e / V) + e % V;
+          if (s > 0) v += s_sum[to];
+          if (s == held - 1) part[to] = v;
+          else s_sum[to] = v;
+        }
       }
     }
   }
@@ -460,53 +682,136 @@ __global__ void __launch_bounds__(kSumCols* kSumRows) sol_residual_norm_sum_b_ke
   }
 }
 
-int threads_per_row(int C, int elems) { return (C + 32 * elems - 1) / (32 * elems) * 32; }
-int rows_per_block(int tpr) { return tpr >= 256 ? 1 : 256 / tpr; }
+// How a row is laid over threads: the channels per thread that pad a row least, at a tie the larger,
+// which halves the shuffles per value; rows of more than 2048 channels always take 16, since a
+// block of 8-channel threads would not leave them registers enough.
+struct Shape {
+  int elems, tpr, rpb, threads;
+};
+Shape shape_of(int C) {
+  auto per_row = [C](int e) {
+    const int n = (C + e - 1) / e;
+    if (n >= 32) return (n + 31) / 32 * 32;
+    int t = 1;
+    while (t < n) t *= 2;
+    return t;
+  };
+  Shape s;
+  s.elems = C > 2048 || 16 * per_row(16) <= 8 * per_row(8) ? 16 : 8;
+  s.tpr = per_row(s.elems);
+  s.rpb = s.tpr >= 256 ? 1 : 256 / s.tpr;
+  s.threads = s.tpr * s.rpb;
+  return s;
+}
+size_t row_bytes(const Shape& s, int bytes) { return static_cast<size_t>(s.threads) * s.elems * bytes; }
 
-template <typename T, int V>
-cudaError_t launch_fwd(const NormArgs& a, cudaStream_t stream) {
-  const int tpr = threads_per_row(a.C, kFwdElems), rpb = rows_per_block(tpr), nt = tpr * rpb;
-  const long long blocks = (static_cast<long long>(a.B) * a.T + rpb - 1) / rpb;
-  const int grid = static_cast<int>(blocks < 0x7fffffffll ? blocks : 0x7fffffffll);
-  if (nt <= 256) sol_residual_norm_kernel<T, V, kFwdElems, 256><<<grid, nt, 0, stream>>>(a, tpr);
-  else sol_residual_norm_kernel<T, V, kFwdElems, 512><<<grid, nt, 0, stream>>>(a, tpr);
+template <typename T, int V, int E, bool RING, bool FULL, int MAXT>
+cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t stream) {
+  // rows side by side in a block: as many as share an SM, unless the batch entries have fewer
+  const long long share = (static_cast<long long>(a.B) * a.T + num_sms - 1) / num_sms;
+  const size_t row = static_cast<size_t>(s.tpr) * E * sizeof(T) * (a.y != nullptr ? 2 : 1) * (RING ? 2 : 0);
+  const size_t products = static_cast<size_t>(s.tpr) * E * 12;
+  s.rpb = MAXT / s.tpr;
+  if (s.tpr > 32 && s.rpb > 15) s.rpb = 15;
+  if (row > 0 && s.rpb > static_cast<long long>((kSmemMax - 10240 - products) / row))
+    s.rpb = static_cast<int>((kSmemMax - 10240 - products) / row);
+  if (s.rpb > a.T) s.rpb = a.T;
+  if (s.rpb > share) s.rpb = static_cast<int>(share);
+  if (s.tpr < 32) s.rpb = (s.rpb * s.tpr + 31) / 32 * 32 / s.tpr;  // whole warps
+  s.threads = s.tpr * s.rpb;
+  const size_t smem = products + row * s.rpb;
+  const long long per_sm = static_cast<long long>(MAXT / s.threads) < 1 ? 1 : MAXT / s.threads;
+  long long chunks = per_sm * num_sms / a.B, most = (a.T + s.rpb - 1) / s.rpb;
+  if (chunks > most) chunks = most;
+  if (chunks < 1) chunks = 1;
+  if (smem > 36 * 1024) {  // beyond 48 KB with the static part
+    const cudaError_t e = cudaFuncSetAttribute(sol_residual_norm_kernel<T, V, E, RING, FULL, MAXT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  sol_residual_norm_kernel<T, V, E, RING, FULL, MAXT>
+      <<<static_cast<unsigned>(a.B * chunks), s.threads, smem, stream>>>(a, s.tpr, static_cast<int>(chunks));
   return cudaGetLastError();
 }
+template <typename T, int V, bool FULL>
+cudaError_t launch_fwd(const NormArgs& a, const Shape& s, int num_sms, cudaStream_t stream) {
+  if constexpr (V > 1) {
+    // two rows in the ring; fp32 rows of more than 7680 channels with a branch leave it no room and are read directly
+    if (static_cast<size_t>(s.tpr) * s.elems * (12 + 2 * sizeof(T) * (a.y != nullptr ? 2 : 1)) <= kSmemMax - 10240)
+      return s.elems == 8 ? launch_fwd_k<T, V, 8, true, FULL, 1024>(a, s, num_sms, stream)
+                          : launch_fwd_k<T, V, 16, true, FULL, 1024>(a, s, num_sms, stream);
+  }
+  return s.elems == 8 ? launch_fwd_k<T, V, 8, false, FULL, 1024>(a, s, num_sms, stream)
+                      : launch_fwd_k<T, V, 16, false, FULL, 1024>(a, s, num_sms, stream);
+}
 
-template <typename T, int V>
-cudaError_t launch_bwd(const NormBwdArgs& a, cudaStream_t stream) {
-  const int tpr = threads_per_row(a.C, kBwdElems), rpb = rows_per_block(tpr), nt = tpr * rpb;
-  const int grid = a.fwd.B * a.chunks;
-  if (nt <= 256) sol_residual_norm_bwd_kernel<T, V, kBwdElems, 256><<<grid, nt, 0, stream>>>(a, tpr);
-  else if (nt <= 512) sol_residual_norm_bwd_kernel<T, V, kBwdElems, 512><<<grid, nt, 0, stream>>>(a, tpr);
-  else sol_residual_norm_bwd_kernel<T, V, kBwdElems, 1024><<<grid, nt, 0, stream>>>(a, tpr);
+template <typename T, int V, int E, bool RING, bool FULL, int MAXT, int MINB>
+cudaError_t launch_bwd_k(const NormBwdArgs& a, const Shape& s, int tensors, cudaStream_t stream) {
+  size_t smem = row_bytes(s, 8 + (RING ? 2 : 0) * tensors * static_cast<int>(sizeof(T)));
+  if (s.rpb > 1 && smem < 12u * a.C) smem = 12u * a.C;  // the sums of a block's rows take the slots' place
+  if (smem > 36 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(sol_residual_norm_bwd_kernel<T, V, E, RING, FULL, MAXT, MINB>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  sol_residual_norm_bwd_kernel<T, V, E, RING, FULL, MAXT, MINB><<<a.fwd.B * a.chunks, s.threads, smem, stream>>>(a, s.tpr);
   return cudaGetLastError();
+}
+template <typename T, int V, int E, bool RING, bool FULL>
+cudaError_t launch_bwd_t(const NormBwdArgs& a, const Shape& s, int tensors, cudaStream_t stream) {
+  if constexpr (E == 8) return launch_bwd_k<T, V, E, RING, FULL, 256, 3>(a, s, tensors, stream);
+  else if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 2>(a, s, tensors, stream);
+  else return launch_bwd_k<T, V, E, RING, FULL, 512, 1>(a, s, tensors, stream);
+}
+template <typename T, int V, bool FULL>
+cudaError_t launch_bwd(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
+  const int tensors = 2 + (a.fwd.y != nullptr) + (a.dx_out != nullptr);
+  if constexpr (V > 1) {
+    // two rows in the ring where they fit; fp32 rows of more than 5632 channels are read directly
+    if (row_bytes(s, 8 + 2 * tensors * static_cast<int>(sizeof(T))) <= kSmemMax - 8192)
+      return s.elems == 8 ? launch_bwd_t<T, V, 8, true, FULL>(a, s, tensors, stream)
+                          : launch_bwd_t<T, V, 16, true, FULL>(a, s, tensors, stream);
+  }
+  return s.elems == 8 ? launch_bwd_t<T, V, 8, false, FULL>(a, s, tensors, stream)
+                      : launch_bwd_t<T, V, 16, false, FULL>(a, s, tensors, stream);
 }
 
 }  // namespace
 
 int norm_bwd_chunks(int B, int T, int C) {
-  const int rpb = rows_per_block(threads_per_row(C, kBwdElems));
-  const int most = (T + rpb - 1) / rpb;
-  const int want = kNormBwdBlocks / B > 1 ? kNormBwdBlocks / B : 1;
+  const Shape s = shape_of(C);
+  const int most = (T + s.rpb - 1) / s.rpb;
+  const int blocks = s.threads > 256 ? kNormBwdBlocks / 4 : s.elems == 16 ? kNormBwdBlocks / 2 : kNormBwdBlocks * 3 / 4;
+  const int want = blocks / B > 1 ? blocks / B : 1;
   return most < want ? most : want;
 }
-size_t norm_bwd_part_floats(int B, int T, int C) {
-  return static_cast<size_t>(B) * norm_bwd_chunks(B, T, C) * rows_per_block(threads_per_row(C, kBwdElems)) * 3 * C;
-}
+size_t norm_bwd_part_floats(int B, int T, int C) { return static_cast<size_t>(B) * norm_bwd_chunks(B, T, C) * 3 * C; }
 
-cudaError_t launch_residual_norm(const NormArgs& a, cudaStream_t stream) {
-  if (a.bf16) return a.vec ? launch_fwd<__nv_bfloat16, 8>(a, stream) : launch_fwd<__nv_bfloat16, 1>(a, stream);
-  return a.vec ? launch_fwd<float, 4>(a, stream) : launch_fwd<float, 1>(a, stream);
+cudaError_t launch_residual_norm(const NormArgs& a, int num_sms, cudaStream_t stream) {
+  const Shape s = shape_of(a.C);
+  const bool full = a.C == s.tpr * s.elems && s.tpr >= 32;
+  if (a.bf16) {
+    if (!a.vec) return launch_fwd<__nv_bfloat16, 1, false>(a, s, num_sms, stream);
+    return full ? launch_fwd<__nv_bfloat16, 8, true>(a, s, num_sms, stream) : launch_fwd<__nv_bfloat16, 8, false>(a, s, num_sms, stream);
+  }
+  if (!a.vec) return launch_fwd<float, 1, false>(a, s, num_sms, stream);
+  return full ? launch_fwd<float, 4, true>(a, s, num_sms, stream) : launch_fwd<float, 4, false>(a, s, num_sms, stream);
 }
 
 cudaError_t launch_residual_norm_bwd(const NormBwdArgs& a, cudaStream_t stream) {
   const NormArgs& f = a.fwd;
+  const Shape s = shape_of(a.C);
+  const bool full = a.C == s.tpr * s.elems && s.tpr >= 32;
   cudaError_t e;
-  if (f.bf16) e = f.vec ? launch_bwd<__nv_bfloat16, 8>(a, stream) : launch_bwd<__nv_bfloat16, 1>(a, stream);
-  else e = f.vec ? launch_bwd<float, 4>(a, stream) : launch_bwd<float, 1>(a, stream);
+  if (f.bf16) {
+    e = !f.vec ? launch_bwd<__nv_bfloat16, 1, false>(a, s, stream)
+        : full ? launch_bwd<__nv_bfloat16, 8, true>(a, s, stream) : launch_bwd<__nv_bfloat16, 8, false>(a, s, stream);
+  } else {
+    e = !f.vec ? launch_bwd<float, 1, false>(a, s, stream)
+        : full ? launch_bwd<float, 4, true>(a, s, stream) : launch_bwd<float, 4, false>(a, s, stream);
+  }
   if (e != cudaSuccess || a.part == nullptr) return e;
-  const int slots = a.chunks * rows_per_block(threads_per_row(a.C, kBwdElems));
+  const int slots = a.chunks;
   const dim3 block(kSumCols, kSumRows);
   const unsigned cols = (a.C + kSumCols - 1) / kSumCols;
   sol_residual_norm_sum_kernel<<<dim3(cols, f.B), block, 0, stream>>>(a, slots);
