@@ -1,6 +1,7 @@
 // C ABI of the Sol-Attn forward (declared in include/sol_attn.h): argument validation on the
 // host, TMA tensor-map encoding, and dispatch to the pool, fp32 SIMT and bf16 tcgen05 kernels.
 // Nothing here allocates device memory; every launch goes to the caller's stream.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -41,11 +42,15 @@ sol_status cuda_fail(cudaError_t e, const char* what) {
   return fail(SOL_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Device checks: an sm_100 GPU is current. Returns SOL_OK and its SM count.
+// Device checks: an sm_100 GPU is current. Returns SOL_OK and its SM count, which a device keeps: it is
+// asked once.
 sol_status current_device(int* num_sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev < kDevices && (*num_sms = known[dev].load(std::memory_order_relaxed)) > 0) return SOL_OK;
   int major = 0, minor = 0;
   if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess)
     return cuda_fail(e, "cudaDeviceGetAttribute");
@@ -55,6 +60,7 @@ sol_status current_device(int* num_sms) {
     return fail(SOL_EUNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a (B200)", dev, major, minor);
   if ((e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return cuda_fail(e, "cudaDeviceGetAttribute");
+  if (dev < kDevices) known[dev].store(*num_sms, std::memory_order_relaxed);
   return SOL_OK;
 }
 
