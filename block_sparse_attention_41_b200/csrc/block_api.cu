@@ -112,14 +112,14 @@ sol_status make_operand_map(CUtensorMap* m, const void* base, int rows, int inne
   return make_map2d(m, base, inner, rows, 64, mn ? 64 : tile_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// out [Mo, No] = A . B over Ko, by tiles of 128 x tile_n. A lies in memory as [Mo, Ko] or, a_mn, as
+// out [Mo, No] = A . B over Ko. A lies in memory as [Mo, Ko] or, a_mn, as
 // [Ko, Mo]; B as [No, Ko] or, b_mn, as [Ko, No].
 sol_status run_gemm(sol::GemmArgs& a, const void* A, const void* Bm, void* out, void* z, cudaStream_t stream) {
-  a.tile_n = sol::linear_tile_n(a.Mo, a.No, a.num_sms);
+  a.tile = sol::linear_tile(a.Mo, a.No, a.num_sms);
   a.store_z = z != nullptr;
   sol_status st;
   if ((st = make_operand_map(&a.maps[0], A, a.a_mn ? a.Ko : a.Mo, a.a_mn ? a.Mo : a.Ko, a.a_mn, 128)) != SOL_OK) return st;
-  if ((st = make_operand_map(&a.maps[1], Bm, a.b_mn ? a.Ko : a.No, a.b_mn ? a.No : a.Ko, a.b_mn, a.tile_n)) != SOL_OK) return st;
+  if ((st = make_operand_map(&a.maps[1], Bm, a.b_mn ? a.Ko : a.No, a.b_mn ? a.No : a.Ko, a.b_mn, a.tile.n / a.tile.ctas)) != SOL_OK) return st;
   if ((st = make_map2d(&a.maps[2], out, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK) return st;
   if ((st = make_map2d(&a.maps[3], z != nullptr ? z : out, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK) return st;
   const cudaError_t e = sol::launch_linear_gemm(a, stream);

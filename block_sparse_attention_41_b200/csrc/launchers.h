@@ -190,14 +190,17 @@ cudaError_t launch_rope_tables(const RopeTableArgs& a, cudaStream_t stream);
 enum : int { ACT_NONE = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_SILU = 3 };
 constexpr int kFewRows = 128;  // up to here the forward takes the kernel for few rows
 constexpr int kDzBlocks = 1184;  // blocks of the dz pass: 8 per SM
-int linear_tile_n(int Mo, int No, int num_sms);  // output columns per tile: 256, 128 or 64
+struct GemmTile {
+  int ctas, n;  // a tile is 128 ctas x n outputs on a pair of SMs or one
+};
+GemmTile linear_tile(int Mo, int No, int num_sms);
 int linear_few_tile(int M);                      // tokens per tile of the kernel for few rows
 int linear_dz_chunks(int M, int N);              // row blocks of the dz pass, one partial column sum each
 struct GemmArgs {
   CUtensorMap maps[4];  // A, B (boxes as launch_linear_gemm's tiles want them), out, z
   int Mo, No, Ko;       // output rows, columns, reduction
   bool a_mn, b_mn;      // operand is MN-major: its memory rows run along M or N
-  int tile_n;
+  GemmTile tile;
   const float* bias;    // [No] or null
   const void* residual; // bf16 [Mo, No] or null
   int act;

@@ -8,12 +8,15 @@
 //   dx  [M, K] = dz [M, N] . w [N, K]     dz K-major, w MN-major
 //   dw  [N, K] = dz [M, N]^T . x [M, K]   both MN-major
 //
-// Bound by the tensor pipe for many rows. A persistent CTA per SM walks 128 x TN output tiles; one
-// warp issues TMA loads into a ring of 64-deep slices, one issues the MMAs, eight turn accumulators
-// into outputs. The accumulator is double-buffered in tensor memory, so the epilogue of one tile
-// (bias, activation, residual, rounding, and a TMA store per warp out of swizzled shared memory)
-// runs under the products of the next. TN is 256, 128 or 64: the widest tile moves the fewest
-// operand bytes per product, a narrower one fills the SMs when there are few tiles.
+// Bound by the tensor pipe for many rows. A persistent CTA per SM walks output tiles; one warp issues
+// TMA loads into a ring of 64-deep slices, one issues the MMAs, eight turn accumulators into
+// outputs. The accumulator is double-buffered in tensor memory, so the epilogue of one tile (bias,
+// activation, residual, rounding, and a TMA store per warp out of swizzled shared memory) runs
+// under the products of the next. Large products run on pairs of SMs: a 256 x 256 (or 256 x 128)
+// tile, of which each CTA loads its 128 rows of A and its half of B's rows, and one thread issues the
+// MMAs for both. That halves what shared memory takes in per product for B; a tile of 128 x 256 on one
+// SM is held back there (1.22 PFLOP/s at 33272 x 4096 x 16384). Few tiles go to single SMs, 128 x 128 or
+// 128 x 64 each, to fill more of them.
 //
 // With up to kFewRows rows the layer is bound by reading w once. There the product is taken
 // transposed: 128 rows of w are the M side of the MMA and the tokens its N side, so the ring holds
@@ -23,6 +26,7 @@
 //
 // Every wait is bounded: on expiry the CTA records the timeout in the caller's workspace (where one
 // is given), lets its copies and MMAs in flight end, frees its tensor memory and returns.
+#include <atomic>
 #include <cmath>
 
 #include "device_common.cuh"
@@ -38,14 +42,16 @@ constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr int kEpiBuf = 32 * 64;   // one warp's staging buffer: 32 rows x 32 bf16 columns
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr int kGroupM = 16;        // output row tiles walked together, so a wave of tiles is about square
+constexpr int kGroupRows = 2048;   // output rows walked together, so a wave of tiles is about square
 
-template <int TN>
+// CG: CTAs of a tile, 1 or 2 (a cluster); each has 128 of its rows and TN / CG of B's rows.
+template <int CG, int TN>
 struct GemmCfg {
   static constexpr int A_BYTES = BM * BK * 2;
-  static constexpr int B_BYTES = TN * BK * 2;
+  static constexpr int B_ROWS = TN / CG;
+  static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int NS = 196608 / STAGE;  // 4, 6 or 8 slices of 48, 32 or 24 KB
+  static constexpr int NS = 196608 / STAGE;  // 6 or 8 slices of 32 or 24 KB
   static constexpr int OFF_EPI = NS * STAGE;
   static constexpr int OFF_BAR = OFF_EPI + kEpiWarps * 2 * kEpiBuf;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;  // + alignment of the ring to 1024 bytes
@@ -95,11 +101,20 @@ __device__ __forceinline__ float activation_slope(float z, int act) {
 }
 
 // ---- small PTX helpers of this file -----------------------------------------------------------------
+// CG = 2: the barrier may lie in the other CTA of the pair.
+template <int CG = 1>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+  if constexpr (CG == 1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  }
 }
 __device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
@@ -128,24 +143,81 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+// The address of this CTA's shared memory `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+
+// The tcgen05 operations that differ for a pair of CTAs.
+template <int CG>
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  if constexpr (CG == 1) {
+    tmem_alloc(dst_smem, ncols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  if constexpr (CG == 1) tmem_dealloc(taddr, ncols);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1) {
+    mma_bf16_ss(d_tmem, a_desc, b_desc, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// Arrive on `bar`, of a pair in both CTAs, when the operations issued so far have completed.
+template <int CG>
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  if constexpr (CG == 1) {
+    tc_commit(bar);
+  } else {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(bar), "h"(static_cast<uint16_t>(3))
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// All threads of the CTA, or of the pair.
+template <int CG>
+__device__ __forceinline__ void pair_sync() {
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_arrive_wait();
+}
+
 // Records an expired wait: stops the CTA's other roles and, where there is a workspace, tells the host.
 __device__ __forceinline__ void report(volatile int* abort_flag, uint32_t* ws, uint32_t where) {
   if (ws != nullptr) raise_timeout(abort_flag, ws, where);
   else *abort_flag = 1;
 }
 
-constexpr uint32_t instr_desc(int N, bool a_mn, bool b_mn) {
-  return idesc_bf16_f32(BM, N, b_mn) | (a_mn ? 1u << 15 : 0u);
+constexpr uint32_t instr_desc(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_bf16_f32(M, N, b_mn) | (a_mn ? 1u << 15 : 0u);
 }
 
 // One 64-deep slice of an operand: `rows` rows along its M or N side, starting at r0, reduction from
 // k0. K-major: one box of 64 x rows. MN-major: boxes of 64 (M or N) x 64 (reduction), 8 KB each.
-template <bool MN>
+template <int CG, bool MN>
 __device__ __forceinline__ void load_operand(uint32_t dst, const void* tmap, uint32_t bar, int r0, int rows, int k0) {
   if constexpr (!MN) {
-    tma_load_2d(dst, tmap, bar, k0, r0);
+    tma_load_2d<CG>(dst, tmap, bar, k0, r0);
   } else {
-    for (int i = 0; i < rows / 64; ++i) tma_load_2d(dst + i * 8192, tmap, bar, r0 + 64 * i, k0);
+    for (int i = 0; i < rows / 64; ++i) tma_load_2d<CG>(dst + i * 8192, tmap, bar, r0 + 64 * i, k0);
   }
 }
 template <bool MN>
@@ -156,8 +228,10 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
 template <bool MN>
 constexpr uint32_t kDescStep = MN ? 2048 >> 4 : 32 >> 4;
 
-// Tile number -> (row tile, column tile): kGroupM row tiles at a time, column by column.
+// Tile number -> (row tile, column tile): kGroupRows rows at a time, column by column.
+template <int CG>
 __device__ __forceinline__ void tile_of(const GemmParams& p, int t, int& tm, int& tn) {
+  constexpr int kGroupM = kGroupRows / (CG * BM);
   const int per_group = kGroupM * p.tiles_n;
   const int g = t / per_group, in = t - g * per_group;
   const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
@@ -166,15 +240,15 @@ __device__ __forceinline__ void tile_of(const GemmParams& p, int t, int& tm, int
 }
 
 // ---- many rows ------------------------------------------------------------------------------------
-template <int TN, bool A_MN, bool B_MN>
+template <int CG, int TN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     sol_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
                       const __grid_constant__ GemmParams p) {
-  using C = GemmCfg<TN>;
+  using C = GemmCfg<CG, TN>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t sb = (raw + 1023u) & ~1023u;
+  const uint32_t sb = (raw + 1023u) & ~1023u;  // the same offset in both CTAs of a pair
   uint8_t* smem = smem_raw + (sb - raw);
   const uint32_t bars = sb + C::OFF_BAR;
   const uint32_t bar_full = bars, bar_empty = bars + 8 * C::NS, bar_acc = bars + 16 * C::NS,
@@ -183,62 +257,71 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 16 * C::NS + 44);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CG == 1 ? 0u : cluster_rank();  // rank 0 issues the MMAs of a pair
   if (tid == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, 1);   // of a pair only rank 0's, for the bytes of both
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar_acc + 8 * a, 1);
-      mbar_init(bar_free + 8 * a, kEpiWarps);
+      mbar_init(bar_free + 8 * a, CG * kEpiWarps);  // of a pair only rank 0's
     }
     mbar_init(bar_drain, 1);
     fence_mbar_init();
     *s_abort = 0;
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
-    tmem_relinquish();
-  }
+  if (warp == 1) pair_tmem_alloc<CG>(smem_u32(s_tmem), C::TMEM_COLS);
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) __syncthreads();
+  pair_sync<CG>();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int tiles = p.tiles_m * p.tiles_n;
+  const int tiles = p.tiles_m * p.tiles_n, first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == 0) {
     if (lane == 0) {
       tma_prefetch_desc(&map_a);
       tma_prefetch_desc(&map_b);
+      const uint32_t full0 = CG == 1 ? bar_full : in_cta(bar_full, 0);
       uint32_t g = 0;  // slices loaded so far
       int w = WAIT_OK;
-      for (int t = blockIdx.x; t < tiles && w == WAIT_OK; t += gridDim.x) {
+      for (int t = first; t < tiles && w == WAIT_OK; t += step) {
         int tm, tn;
-        tile_of(p, t, tm, tn);
+        tile_of<CG>(p, t, tm, tn);
+        const int row0 = tm * CG * BM + static_cast<int>(rank) * BM, col0 = tn * TN + static_cast<int>(rank) * C::B_ROWS;
         for (int k = 0; k < p.nk; ++k, ++g) {
           const uint32_t s = g % C::NS;
           if (g >= C::NS) {
             w = mbar_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort, kWaitLimitNs);
             if (w != WAIT_OK) break;
           }
-          mbar_arrive_expect_tx(bar_full + 8 * s, C::STAGE);
+          // rank 1's bytes may land first: its slice is free, so the barrier is already in this phase
+          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, CG * C::STAGE);
           const uint32_t dst = sb + s * C::STAGE;
-          load_operand<A_MN>(dst, &map_a, bar_full + 8 * s, tm * BM, BM, k * BK);
-          load_operand<B_MN>(dst + C::A_BYTES, &map_b, bar_full + 8 * s, tn * TN, TN, k * BK);
+          load_operand<CG, A_MN>(dst, &map_a, full0 + 8 * s, row0, BM, k * BK);
+          load_operand<CG, B_MN>(dst + C::A_BYTES, &map_b, full0 + 8 * s, col0, C::B_ROWS, k * BK);
         }
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_PRODUCER);
-      // no copy may be in flight when shared memory is released: the last use of every slice
-      for (uint32_t i = g > C::NS ? g - C::NS : 0; i < g; ++i)
-        mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, kWaitLimitNs);
+      // No copy may be in flight when shared memory is released: the last use of every slice. Rank 1 cannot
+      // see its own land: rank 0 does, before both meet at the end; after an abort it waits a while.
+      if (rank == 0) {
+        for (uint32_t i = g > C::NS ? g - C::NS : 0; i < g; ++i)
+          mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, kWaitLimitNs);
+      } else if (w != WAIT_OK) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
+        }
+      }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = instr_desc(TN, A_MN, B_MN);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = instr_desc(CG * BM, TN, A_MN, B_MN);
       const uint64_t da0 = operand_desc<A_MN>(sb), db0 = operand_desc<B_MN>(sb + C::A_BYTES);
       uint32_t g = 0, it = 0;
       int w = WAIT_OK;
-      for (int t = blockIdx.x; t < tiles && w == WAIT_OK; t += gridDim.x, ++it) {
+      for (int t = first; t < tiles && w == WAIT_OK; t += step, ++it) {
         const uint32_t acc = it & 1u;
         if (it >= 2) {
           w = mbar_wait(bar_free + 8 * acc, (it / 2 - 1u) & 1u, s_abort, kWaitLimitNs);
@@ -253,14 +336,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint64_t da = da0 + ((s * C::STAGE) >> 4), db = db0 + ((s * C::STAGE) >> 4);
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16_ss(tmem + acc * TN, da + kk * kDescStep<A_MN>, db + kk * kDescStep<B_MN>, idesc,
-                        (k > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(bar_empty + 8 * s);
+            pair_mma<CG>(tmem + acc * TN, da + kk * kDescStep<A_MN>, db + kk * kDescStep<B_MN>, idesc,
+                         (k > 0 || kk > 0) ? 1u : 0u);
+          pair_commit<CG>(bar_empty + 8 * s);
         }
-        if (w == WAIT_OK) tc_commit(bar_acc + 8 * acc);
+        if (w == WAIT_OK) pair_commit<CG>(bar_acc + 8 * acc);
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_MMA);
-      tc_commit(bar_drain);  // no MMA may be in flight when tensor memory is freed
+      pair_commit<CG>(bar_drain);  // no MMA may be in flight when tensor memory is freed
       mbar_wait(bar_drain, 0, nullptr, kWaitLimitNs);
     }
     __syncwarp();
@@ -270,16 +353,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t buf0 = sb + C::OFF_EPI + ew * 2 * kEpiBuf;
     const uint32_t swz = (lane >> 1) & 3;  // 64-byte swizzle: 16-byte chunk c of row r sits at c ^ ((r / 2) % 4)
+    const uint32_t free0 = CG == 1 ? bar_free : in_cta(bar_free, 0);
     uint32_t it = 0, stores = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    for (int t = first; t < tiles; t += step, ++it) {
       int tm, tn;
-      tile_of(p, t, tm, tn);
+      tile_of<CG>(p, t, tm, tn);
       const uint32_t acc = it & 1u;
       const int w = mbar_wait(bar_acc + 8 * acc, (it / 2) & 1u, s_abort, kWaitLimitNs);
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
       if (__any_sync(0xffffffffu, w != WAIT_OK)) break;
       tc_fence_after();
-      const int row0 = tm * BM + q * 32, row = row0 + lane;
+      const int row0 = (tm * CG + static_cast<int>(rank)) * BM + q * 32, row = row0 + lane;
       const bool live = row < p.Mo;
 #pragma unroll 1
       for (int c = c_lo; c < c_lo + TN / 2; c += 32) {
@@ -347,15 +431,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_free + 8 * acc);
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive(bar_free + 8 * acc);
+        else mbar_arrive_cluster(free0 + 8 * acc);
+      }
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) __syncthreads();
+  pair_sync<CG>();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == 1) pair_tmem_dealloc<CG>(tmem, C::TMEM_COLS);
 }
 
 // ---- few rows --------------------------------------------------------------------------------------
@@ -443,7 +531,7 @@ __global__ void __launch_bounds__(kFewThreads)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = instr_desc(TT, false, false);
+      constexpr uint32_t idesc = instr_desc(BM, TT, false, false);
       const uint64_t da0 = operand_desc<false>(sb), db0 = operand_desc<false>(sb + C::A_BYTES);
       uint32_t g = 0;
       int w = WAIT_OK;
@@ -592,31 +680,54 @@ __global__ void __launch_bounds__(512) sol_linear_db_kernel(const float* __restr
   }
 }
 
-template <int TN, bool A_MN, bool B_MN>
+// A kernel's dynamic shared memory is allowed once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  constexpr int kDevices = 64;
+  static std::atomic<bool> done[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < kDevices && done[dev].load(std::memory_order_relaxed))) return e;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kDevices) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+template <int CG, int TN, bool A_MN, bool B_MN>
 cudaError_t launch_gemm_t(const GemmArgs& a, GemmParams p, cudaStream_t stream) {
-  using C = GemmCfg<TN>;
-  p.tiles_m = (a.Mo + BM - 1) / BM;
+  using C = GemmCfg<CG, TN>;
+  p.tiles_m = (a.Mo + CG * BM - 1) / (CG * BM);
   p.tiles_n = (a.No + TN - 1) / TN;
-  const cudaError_t e = cudaFuncSetAttribute(sol_linear_kernel<TN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::SMEM);
+  const cudaError_t e = allow_smem<sol_linear_kernel<CG, TN, A_MN, B_MN>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-  const int grid = static_cast<int>(tiles < a.num_sms ? tiles : a.num_sms);
-  sol_linear_kernel<TN, A_MN, B_MN><<<grid, kGemmThreads, C::SMEM, stream>>>(a.maps[0], a.maps[1], a.maps[2], a.maps[3], p);
-  return cudaGetLastError();
+  const int units = a.num_sms / CG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CG * static_cast<int>(tiles < units ? tiles : units));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, sol_linear_kernel<CG, TN, A_MN, B_MN>, a.maps[0], a.maps[1], a.maps[2], a.maps[3], p);
 }
 
 template <bool A_MN, bool B_MN>
 cudaError_t launch_gemm_n(const GemmArgs& a, const GemmParams& p, cudaStream_t stream) {
-  if (a.tile_n == 256) return launch_gemm_t<256, A_MN, B_MN>(a, p, stream);
-  if (a.tile_n == 128) return launch_gemm_t<128, A_MN, B_MN>(a, p, stream);
-  return launch_gemm_t<64, A_MN, B_MN>(a, p, stream);
+  if (a.tile.ctas == 2)
+    return a.tile.n == 256 ? launch_gemm_t<2, 256, A_MN, B_MN>(a, p, stream) : launch_gemm_t<2, 128, A_MN, B_MN>(a, p, stream);
+  return a.tile.n == 128 ? launch_gemm_t<1, 128, A_MN, B_MN>(a, p, stream) : launch_gemm_t<1, 64, A_MN, B_MN>(a, p, stream);
 }
 
 template <int TT>
 cudaError_t launch_few_t(const FewArgs& a, const FewParams& p, cudaStream_t stream) {
   using C = FewCfg<TT>;
-  const cudaError_t e = cudaFuncSetAttribute(sol_linear_few_kernel<TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t e = allow_smem<sol_linear_few_kernel<TT>>(C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.N + BM - 1) / BM * p.split);
@@ -635,18 +746,18 @@ cudaError_t launch_few_t(const FewArgs& a, const FewParams& p, cudaStream_t stre
 
 }  // namespace
 
-int linear_tile_n(int Mo, int No, int num_sms) {
-  // time of the last SM to finish, in columns of a 256-wide tile's rate: a narrower tile re-reads more
+GemmTile linear_tile(int Mo, int No, int num_sms) {
+  // time of the last SM to finish, in columns of a 256 x 256 pair tile's rate: a smaller tile re-reads more
   // operand bytes per product and runs at a lower rate
-  const struct { int tn; double cost; } options[] = {{256, 256.0}, {128, 150.0}, {64, 100.0}};
-  int best = 256;
+  const struct { GemmTile tile; double cost; } options[] = {{{2, 256}, 256.0}, {{2, 128}, 150.0}, {{1, 128}, 160.0}, {{1, 64}, 105.0}};
+  GemmTile best = options[0].tile;
   double least = 0.0;
   for (const auto& o : options) {
-    const double tiles = std::ceil(Mo / 128.0) * std::ceil(No / static_cast<double>(o.tn));
-    const double t = std::ceil(tiles / num_sms) * o.cost;
-    if (o.tn == 256 || t < least) {
+    const double tiles = std::ceil(Mo / (128.0 * o.tile.ctas)) * std::ceil(No / static_cast<double>(o.tile.n));
+    const double t = std::ceil(tiles / (num_sms / o.tile.ctas)) * o.cost;
+    if (least == 0.0 || t < least) {
       least = t;
-      best = o.tn;
+      best = o.tile;
     }
   }
   return best;

@@ -97,6 +97,24 @@ def test_many_tiles_per_sm_and_a_deep_ring():
         same_bits(db, rb, f"db {M} {N} {K}")
 
 
+@pytest.mark.parametrize("M,N,K", [(4104, 4096, 136), (4104, 136, 4096), (136, 4104, 4096), (4000, 4360, 72), (2304, 20000, 8)])
+def test_many_large_tiles(M, N, K):
+    # enough outputs in one of the three products for tiles of two SMs, ragged at the ends
+    g = _gen(M, N, K, 6)
+    x, w, dy = ints(g, -2, 2, M, K), ints(g, -2, 2, N, K), ints(g, -2, 2, M, N)
+    res = ints(g, -9, 9, M, N)
+    bias = torch.randint(-5, 6, (N,), generator=g, device="cuda").float()
+    out, z = sa.sol_attn_linear(x, w, bias, residual=res, want_z=True)
+    ref, rz = bo.linear(_np(x), _np(w), _np(bias), "none", _np(res))
+    same_bits(out, ref, "out")
+    same_bits(z, rz, "z")
+    dx, dw, db = sa.sol_attn_linear_bwd(dy, x, w)
+    rx, rw, rb = bo.linear_bwd(_np(dy), _np(x), _np(w))
+    same_bits(dx, rx, "dx")
+    same_bits(dw, rw, "dw")
+    same_bits(db, rb, "db")
+
+
 def sum_error(K):
     return 17 * (K / 16 + 1) * 2.0 ** -23
 
