@@ -28,6 +28,7 @@
 // is given), lets its copies and MMAs in flight end, frees its tensor memory and returns.
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "launchers.h"
@@ -68,35 +69,82 @@ struct GemmParams {
   uint32_t* ws;  // error words, or null
 };
 
-// ---- activations and their slopes -----------------------------------------------------------------
-// tanh-form gelu: z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3). With e = 2^(-2 u log2 e), both
-// ends are right without a branch: e = inf gives 0, e = 0 gives z.
-__device__ __forceinline__ float sigmoid_of(float x) { return __fdividef(1.0f, 1.0f + ex2_approx(-1.4426950408889634f * x)); }
-// __fdividef(1, d) is 0 for d above 2^126, which is what the sigmoid tends to there.
+// ---- activations and their slopes, two values at a time ------------------------------------------------
+__device__ __forceinline__ f2 dup2(float v) { return pack2(v, v); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ f2 ex2_2(f2 x) {
+  const float2 v = unpack2(x);
+  return pack2(ex2_approx(v.x), ex2_approx(v.y));
+}
+__device__ __forceinline__ f2 rcp_2(f2 x) {
+  const float2 v = unpack2(x);
+  return pack2(rcp_approx(v.x), rcp_approx(v.y));
+}
+// 1 / (1 + 2^x): both ends are right without a branch, 2^x = inf gives 0.
+__device__ __forceinline__ f2 sigmoid_ex2(f2 x) { return rcp_2(add2(ex2_2(x), dup2(1.0f))); }
 
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case ACT_GELU_TANH: return z * sigmoid_of(1.5957691216057308f * fmaf(0.044715f * z * z, z, z));
-    case ACT_SILU: return z * sigmoid_of(z);
-    default: return z;
+// The normal distribution's Phi(z), with e = exp(-z^2 / 2), which its density shares. From erfc(x) =
+// (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0, of Abramowitz and Stegun, 7.1.26
+// (after Hastings), off by at most 1.5e-7: half of that here, a bf16 step of values near 1 is 2e-3.
+__device__ __forceinline__ f2 normal_cdf(f2 z, f2& e) {
+  e = ex2_2(mul2(mul2(z, z), dup2(-0.72134752044448170f)));
+  const float2 v = unpack2(z);
+  const f2 t = rcp_2(fma2(pack2(fabsf(v.x), fabsf(v.y)), dup2(0.3275911f * 0.70710678118654752f), dup2(1.0f)));
+  f2 q = fma2(t, dup2(0.5f * 1.061405429f), dup2(0.5f * -1.453152027f));
+  q = fma2(q, t, dup2(0.5f * 1.421413741f));
+  q = fma2(q, t, dup2(0.5f * -0.284496736f));
+  q = fma2(q, t, dup2(0.5f * 0.254829592f));
+  const float2 h = unpack2(mul2(mul2(q, t), e));  // the tail beyond |z|
+  return pack2(v.x < 0.f ? h.x : 1.0f - h.x, v.y < 0.f ? h.y : 1.0f - h.y);
+}
+// -2 log2(e) sqrt(2 / pi) (z + 0.044715 z^3): the tanh form of gelu is z times the sigmoid of it
+__device__ __forceinline__ f2 gelu_tanh_arg(f2 z, f2 z2) {
+  return mul2(z, fma2(z2, dup2(-2.3022082f * 0.044715f), dup2(-2.3022082f)));
+}
+
+template <int ACT>
+__device__ __forceinline__ f2 activate(f2 z) {
+  if constexpr (ACT == ACT_GELU) {
+    f2 e;
+    return mul2(z, normal_cdf(z, e));
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    return mul2(z, sigmoid_ex2(gelu_tanh_arg(z, mul2(z, z))));
+  } else if constexpr (ACT == ACT_SILU) {
+    return mul2(z, sigmoid_ex2(mul2(z, dup2(-1.4426950408889634f))));
+  } else {
+    return z;
   }
 }
-__device__ __forceinline__ float activation_slope(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ f2 activation_slope(f2 z) {
+  if constexpr (ACT == ACT_GELU) {
+    f2 e;
+    const f2 c = normal_cdf(z, e);
+    return fma2(mul2(z, dup2(0.39894228040143268f)), e, c);
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    const f2 z2 = mul2(z, z), s = sigmoid_ex2(gelu_tanh_arg(z, z2));
+    // s + z s (1 - s) 2 sqrt(2 / pi) (1 + 3 0.044715 z^2)
+    const f2 g = mul2(z, fma2(z2, dup2(1.5957691216057308f * 3.0f * 0.044715f), dup2(1.5957691216057308f)));
+    return fma2(mul2(g, s), fma2(s, dup2(-1.0f), dup2(1.0f)), s);
+  } else if constexpr (ACT == ACT_SILU) {
+    const f2 s = sigmoid_ex2(mul2(z, dup2(-1.4426950408889634f)));
+    return mul2(s, fma2(z, fma2(s, dup2(-1.0f), dup2(1.0f)), dup2(1.0f)));
+  } else {
+    return dup2(1.0f);
+  }
+}
+// f(its constant) for the activation of a call
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
   switch (act) {
-    case ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-             z * 0.39894228040143268f * ex2_approx(-0.72134752044448170f * z * z);
-    case ACT_GELU_TANH: {
-      const float z2 = z * z;
-      const float s = sigmoid_of(1.5957691216057308f * fmaf(0.044715f * z2, z, z));
-      return s + z * s * (1.0f - s) * 1.5957691216057308f * fmaf(3.0f * 0.044715f, z2, 1.0f);
-    }
-    case ACT_SILU: {
-      const float s = sigmoid_of(z);
-      return s * fmaf(z, 1.0f - s, 1.0f);
-    }
-    default: return 1.0f;
+    case ACT_GELU: f(std::integral_constant<int, ACT_GELU>{}); break;
+    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
+    case ACT_SILU: f(std::integral_constant<int, ACT_SILU>{}); break;
+    default: break;
   }
 }
 
@@ -359,27 +407,48 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int tm, tn;
       tile_of<CG>(p, t, tm, tn);
       const uint32_t acc = it & 1u;
+      const int row0 = (tm * CG + static_cast<int>(rank)) * BM + q * 32, row = row0 + lane;
+      // the residual's values of a chunk of 32 columns are asked for one chunk ahead
+      const bool live = p.residual != nullptr && row < p.Mo;
+      const __nv_bfloat16* res = p.residual + static_cast<size_t>(row) * p.No + tn * TN;
+      uint4 ahead[4];
+      auto ask = [&](int c) {
+        if (live && c < c_lo + TN / 2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (tn * TN + c + 8 * i < p.No) ahead[i] = __ldg(reinterpret_cast<const uint4*>(res + c + 8 * i));
+        }
+      };
+      ask(c_lo);
       const int w = mbar_wait(bar_acc + 8 * acc, (it / 2) & 1u, s_abort, kWaitLimitNs);
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
       if (__any_sync(0xffffffffu, w != WAIT_OK)) break;
       tc_fence_after();
-      const int row0 = (tm * CG + static_cast<int>(rank)) * BM + q * 32, row = row0 + lane;
-      const bool live = row < p.Mo;
 #pragma unroll 1
       for (int c = c_lo; c < c_lo + TN / 2; c += 32) {
         const int col0 = tn * TN + c;
         if (col0 >= p.No) break;  // uniform: the rest of the tile is past the last column
         uint32_t r[32];
         tmem_ld_x32(tmem + lane_base + acc * TN + c, r);
-        auto emit = [&](const CUtensorMap* map, const uint32_t (&pk)[16]) {
+        f2 v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        auto emit = [&](const CUtensorMap* map) {
           const uint32_t buf = buf0 + (stores & 1u) * kEpiBuf;
           if (lane == 0) bulk_wait_read<1>();  // the store before the last one has left this buffer
           __syncwarp();
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((v ^ swz) << 4)),
-                         "r"(pk[4 * v]), "r"(pk[4 * v + 1]), "r"(pk[4 * v + 2]), "r"(pk[4 * v + 3])
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = unpack2(v[4 * i + j]);
+              pk[j] = pack_bf16x2(f.x, f.y);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((i ^ swz) << 4)), "r"(pk[0]),
+                         "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
                          : "memory");
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -388,46 +457,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           ++stores;
         };
-        uint32_t pk[16];
         if (p.bias != nullptr) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            if (col0 + j < p.No) {  // No is a multiple of 8
-              const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col0 + j));
-              r[j] = __float_as_uint(__uint_as_float(r[j]) + b.x);
-              r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) + b.y);
-              r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) + b.z);
-              r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) + b.w);
+          for (int j = 0; j < 8; ++j) {
+            if (col0 + 4 * j < p.No) {  // No is a multiple of 8
+              const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col0 + 4 * j));
+              v[2 * j] = add2(v[2 * j], pack2(b.x, b.y));
+              v[2 * j + 1] = add2(v[2 * j + 1], pack2(b.z, b.w));
             }
           }
         }
-        if (p.store_z) {
+        if (p.store_z) emit(&map_z);
+        with_activation(p.act, [&](auto kind) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-          emit(&map_z, pk);
-        }
-        if (p.act != ACT_NONE) {
+          for (int j = 0; j < 16; ++j) v[j] = activate<decltype(kind)::value>(v[j]);
+        });
+        if (live) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(activate(__uint_as_float(r[j]), p.act));
-        }
-        if (p.residual != nullptr && live) {
-          const __nv_bfloat16* res = p.residual + static_cast<size_t>(row) * p.No + col0;
+          for (int i = 0; i < 4; ++i) {
+            if (col0 + 8 * i < p.No) {
+              const uint32_t wv[4] = {ahead[i].x, ahead[i].y, ahead[i].z, ahead[i].w};
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (col0 + j < p.No) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(res + j));
-              const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                r[j + 2 * i] = __float_as_uint(__uint_as_float(r[j + 2 * i]) + __uint_as_float(wv[i] << 16));
-                r[j + 2 * i + 1] = __float_as_uint(__uint_as_float(r[j + 2 * i + 1]) + __uint_as_float(wv[i] & 0xffff0000u));
-              }
+              for (int j = 0; j < 4; ++j)
+                v[4 * i + j] = add2(v[4 * i + j], pack2(__uint_as_float(wv[j] << 16), __uint_as_float(wv[j] & 0xffff0000u)));
             }
           }
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        emit(&map_out, pk);
+        ask(c + 32);
+        emit(&map_out);
       }
       tc_fence_before();
       __syncwarp();
@@ -591,7 +648,7 @@ __global__ void __launch_bounds__(kFewThreads)
       if (p.bias != nullptr) v += __ldg(p.bias + n);
       const size_t o = static_cast<size_t>(m) * p.N + n;
       if (p.z != nullptr) p.z[o] = __float2bfloat16_rn(v);
-      v = activate(v, p.act);
+      with_activation(p.act, [&](auto kind) { v = unpack2(activate<decltype(kind)::value>(dup2(v))).x; });
       if (p.residual != nullptr) v += __bfloat162float(p.residual[o]);
       p.out[o] = __float2bfloat16_rn(v);
     }
@@ -605,52 +662,55 @@ __global__ void __launch_bounds__(kFewThreads)
 // order. HBM-bound: 32 threads side by side cover 256 columns with 16-byte vectors, 8 rows at a time.
 constexpr int kDzCols = 256, kDzRows = 8;
 
+__device__ __forceinline__ void widen_bf16(const uint4& v, f2 (&x)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+}
+
 struct DzParams {
   const __nv_bfloat16* dy;
   const __nv_bfloat16* z;   // null: dz = dy
   __nv_bfloat16* dz;        // null where dz = dy
   float* part;              // [chunks, N] or null
-  int M, N, act, rows;      // rows per block
+  int M, N, rows;           // rows per block
 };
 
+template <int ACT>
 __global__ void __launch_bounds__(kDzCols / 8 * kDzRows) sol_linear_dz_kernel(const __grid_constant__ DzParams p) {
   __shared__ float s[kDzRows][kDzCols + 8];
   const int lane = threadIdx.x, ty = threadIdx.y;
   const int c = blockIdx.x * kDzCols + lane * 8;
   const int r_lo = blockIdx.y * p.rows, r_hi = min(r_lo + p.rows, p.M);
-  float a[8];
+  f2 a[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) a[k] = 0.f;
+  for (int k = 0; k < 4; ++k) a[k] = dup2(0.f);
   if (c < p.N) {
-#pragma unroll 2
+#pragma unroll 4
     for (int r = r_lo + ty; r < r_hi; r += kDzRows) {
       const size_t o = static_cast<size_t>(r) * p.N + c;
       const uint4 g = __ldg(reinterpret_cast<const uint4*>(p.dy + o));
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(gw[k] << 16);
-        v[2 * k + 1] = __uint_as_float(gw[k] & 0xffff0000u);
-      }
-      if (p.z != nullptr) {
-        const uint4 zz = __ldg(reinterpret_cast<const uint4*>(p.z + o));
-        const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
+      f2 v[4];
+      widen_bf16(g, v);
+      if constexpr (ACT != ACT_NONE) {
+        f2 zz[4];
+        widen_bf16(__ldg(reinterpret_cast<const uint4*>(p.z + o)), zz);
+        uint32_t pk[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          v[2 * k] *= activation_slope(__uint_as_float(zw[k] << 16), p.act);
-          v[2 * k + 1] *= activation_slope(__uint_as_float(zw[k] & 0xffff0000u), p.act);
+          v[k] = mul2(v[k], activation_slope<ACT>(zz[k]));
+          const float2 f = unpack2(v[k]);
+          pk[k] = pack_bf16x2(f.x, f.y);
         }
-        *reinterpret_cast<uint4*>(p.dz + o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                         pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        *reinterpret_cast<uint4*>(p.dz + o) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a[k] += v[k];
+      for (int k = 0; k < 4; ++k) a[k] = add2(a[k], v[k]);
     }
   }
   if (p.part == nullptr) return;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s[ty][lane * 8 + k] = a[k];
+  for (int k = 0; k < 4; ++k) *reinterpret_cast<float2*>(&s[ty][lane * 8 + 2 * k]) = unpack2(a[k]);
   __syncthreads();
   const int i = ty * 32 + lane, col = blockIdx.x * kDzCols + i;  // 256 threads: one column each
   if (col < p.N) {
@@ -819,10 +879,15 @@ cudaError_t launch_linear_dz(const void* dy, const void* z, int act, int M, int 
   p.part = part;
   p.M = M;
   p.N = N;
-  p.act = act;
   const int chunks = linear_dz_chunks(M, N);
   p.rows = (M + chunks - 1) / chunks;
-  sol_linear_dz_kernel<<<dim3((N + kDzCols - 1) / kDzCols, chunks), dim3(kDzCols / 8, kDzRows), 0, stream>>>(p);
+  const dim3 grid((N + kDzCols - 1) / kDzCols, chunks), block(kDzCols / 8, kDzRows);
+  switch (act) {
+    case ACT_GELU: sol_linear_dz_kernel<ACT_GELU><<<grid, block, 0, stream>>>(p); break;
+    case ACT_GELU_TANH: sol_linear_dz_kernel<ACT_GELU_TANH><<<grid, block, 0, stream>>>(p); break;
+    case ACT_SILU: sol_linear_dz_kernel<ACT_SILU><<<grid, block, 0, stream>>>(p); break;
+    default: sol_linear_dz_kernel<ACT_NONE><<<grid, block, 0, stream>>>(p); break;
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || part == nullptr) return e;
   sol_linear_db_kernel<<<(N + 31) / 32, dim3(32, 16), 0, stream>>>(part, db, N, chunks);

@@ -28,38 +28,6 @@ constexpr int kMaxWarps = 16;  // of a row
 constexpr int kMaxRows = 16;   // of several warps in a block: 15 named barriers
 constexpr int kSmemMax = 227 * 1024;  // per block
 
-// ---- two fp32 values per register pair ---------------------------------------------------------------
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-  f2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpack2(f2 v) {
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
-  return d;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float sum2(f2 v) {
-  const float2 t = unpack2(v);
-  return t.x + t.y;
-}
-
 // ---- element access ------------------------------------------------------------------------------------
 // A 16-byte vector (V = 8 bf16 or 4 fp32) as V / 2 pairs, and back.
 template <int V>
