@@ -115,8 +115,9 @@ sol_status make_operand_map(CUtensorMap* m, const void* base, int rows, int inne
 // out [Mo, No] = A . B over Ko. A lies in memory as [Mo, Ko] or, a_mn, as
 // [Ko, Mo]; B as [No, Ko] or, b_mn, as [Ko, No].
 sol_status run_gemm(sol::GemmArgs& a, const void* A, const void* Bm, void* out, void* z, cudaStream_t stream) {
-  a.tile = sol::linear_tile(a.Mo, a.No, a.num_sms);
+  a.tile = sol::linear_tile(a.Mo, a.No, a.Ko, a.part != nullptr, a.num_sms);
   a.store_z = z != nullptr;
+  a.out = out;
   sol_status st;
   if ((st = make_operand_map(&a.maps[0], A, a.a_mn ? a.Ko : a.Mo, a.a_mn ? a.Mo : a.Ko, a.a_mn, 128)) != SOL_OK) return st;
   if ((st = make_operand_map(&a.maps[1], Bm, a.b_mn ? a.Ko : a.No, a.b_mn ? a.No : a.Ko, a.b_mn, a.tile.n / a.tile.ctas)) != SOL_OK) return st;
@@ -138,6 +139,7 @@ sol_status linear_sizes(int M, int N, int K, sol_activation act) {
   return SOL_OK;
 }
 
+constexpr int kMaxSms = 148;  // of a B200: the workspace's size is asked for without a device
 constexpr size_t kErrorBytes = 256;  // the workspace's error words, as sol_attn_check_device_error reads them
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -394,6 +396,7 @@ sol_status sol_attn_linear(const void* x, const void* w, const float* bias, cons
   a.bias = bias;
   a.residual = residual;
   a.act = act;
+  a.part = nullptr;
   a.ws = static_cast<uint32_t*>(workspace);
   a.num_sms = sms;
   return run_gemm(a, x, w, out, z, static_cast<cudaStream_t>(stream));
@@ -401,7 +404,7 @@ sol_status sol_attn_linear(const void* x, const void* w, const float* bias, cons
 
 size_t sol_attn_linear_bwd_workspace_bytes(int M, int N, sol_activation act) {
   if (!size_ok(M, 1 << 28) || !size_ok(N, 1 << 28) || act < SOL_ACT_NONE || act > SOL_ACT_SILU) return 0;
-  return kErrorBytes + round256(static_cast<size_t>(sol::linear_dz_chunks(M, N)) * N * 4) +
+  return kErrorBytes + sol::linear_part_bytes(kMaxSms) + round256(static_cast<size_t>(sol::linear_dz_chunks(M, N)) * N * 4) +
          (act == SOL_ACT_NONE ? 0 : round256(static_cast<size_t>(M) * N * 2));
 }
 
@@ -424,8 +427,11 @@ sol_status sol_attn_linear_bwd(const void* dy, const void* x, const void* w, con
   int sms = 0;
   if ((st = current_device(&sms)) != SOL_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kErrorBytes);
-  void* dz = static_cast<uint8_t*>(workspace) + kErrorBytes + round256(static_cast<size_t>(sol::linear_dz_chunks(M, N)) * N * 4);
+  uint8_t* at = static_cast<uint8_t*>(workspace) + kErrorBytes;
+  float* pieces = reinterpret_cast<float*>(at);
+  at += sol::linear_part_bytes(kMaxSms);
+  float* part = reinterpret_cast<float*>(at);
+  void* dz = at + round256(static_cast<size_t>(sol::linear_dz_chunks(M, N)) * N * 4);
   if (act != SOL_ACT_NONE || db != nullptr) {
     const cudaError_t e = sol::launch_linear_dz(dy, z, act, M, N, dz, db != nullptr ? part : nullptr, db, s);
     if (e != cudaSuccess) return cuda_fail(e, "activation gradient launch");
@@ -435,6 +441,7 @@ sol_status sol_attn_linear_bwd(const void* dy, const void* x, const void* w, con
   a.bias = nullptr;
   a.residual = nullptr;
   a.act = sol::ACT_NONE;
+  a.part = sms <= kMaxSms ? pieces : nullptr;
   a.ws = static_cast<uint32_t*>(workspace);
   a.num_sms = sms;
   if (dx != nullptr) {

@@ -192,8 +192,10 @@ constexpr int kFewRows = 128;  // up to here the forward takes the kernel for fe
 constexpr int kDzBlocks = 1184;  // blocks of the dz pass: 8 per SM
 struct GemmTile {
   int ctas, n;  // a tile is 128 ctas x n outputs on a pair of SMs or one
+  int split;    // pieces of the reduction of the last tiles, those past the last whole turn of the SMs
 };
-GemmTile linear_tile(int Mo, int No, int num_sms);
+GemmTile linear_tile(int Mo, int No, int Ko, bool splittable, int num_sms);
+size_t linear_part_bytes(int num_sms);           // accumulators of one tile per SM
 int linear_few_tile(int M);                      // tokens per tile of the kernel for few rows
 int linear_dz_chunks(int M, int N);              // row blocks of the dz pass, one partial column sum each
 struct GemmArgs {
@@ -205,6 +207,8 @@ struct GemmArgs {
   const void* residual; // bf16 [Mo, No] or null
   int act;
   bool store_z;
+  void* out;
+  float* part;          // linear_part_bytes for the pieces of the last tiles, or null; only without an epilogue
   uint32_t* ws;         // error words or null
   int num_sms;
 };

@@ -42,8 +42,16 @@ constexpr int BK = 64;             // reduction depth per slice: one 128-byte sw
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr int kEpiBuf = 32 * 64;   // one warp's staging buffer: 32 rows x 32 bf16 columns
+// A piece of a split tile has at least so many slices; the pieces cost their fp32 tiles through memory and a
+// second kernel.
+constexpr int kPieceSlices = 16;
+constexpr double kPieceCycles = 9000.0;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr int kGroupRows = 2048;   // output rows walked together, so a wave of tiles is about square
+// Output rows walked together, column by column: at least 2048, so that a wave of tiles is about square
+// and its tiles share operands as they stream by; with a short reduction as many as keep their part
+// of A in L2 while B passes (at K = 4096, 4096 rows instead of 2048: 2907 against 2968 us).
+constexpr int kGroupRows = 2048;
+constexpr double kGroupBytes = 33554432.0;
 
 // CG: CTAs of a tile, 1 or 2 (a cluster); each has 128 of its rows and TN / CG of B's rows.
 template <int CG, int TN>
@@ -62,6 +70,9 @@ struct GemmCfg {
 struct GemmParams {
   int Mo, No, nk;  // output rows and columns, reduction slices
   int tiles_m, tiles_n;
+  int group;             // row tiles walked together
+  int whole, split;      // units from `whole` on are pieces of the last tiles, `split` of each
+  float* part;           // their fp32 accumulators, or null
   const float* bias;               // [No] or null
   const __nv_bfloat16* residual;   // [Mo, No] or null
   int act;
@@ -258,6 +269,10 @@ constexpr uint32_t instr_desc(int M, int N, bool a_mn, bool b_mn) {
   return idesc_bf16_f32(M, N, b_mn) | (a_mn ? 1u << 15 : 0u);
 }
 
+__device__ __forceinline__ int ring_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  return mbar_wait(bar, parity, abort_flag, kWaitLimitNs);
+}
+
 // One 64-deep slice of an operand: `rows` rows along its M or N side, starting at r0, reduction from
 // k0. K-major: one box of 64 x rows. MN-major: boxes of 64 (M or N) x 64 (reduction), 8 KB each.
 template <int CG, bool MN>
@@ -276,15 +291,31 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
 template <bool MN>
 constexpr uint32_t kDescStep = MN ? 2048 >> 4 : 32 >> 4;
 
-// Tile number -> (row tile, column tile): kGroupRows rows at a time, column by column.
-template <int CG>
-__device__ __forceinline__ void tile_of(const GemmParams& p, int t, int& tm, int& tn) {
-  constexpr int kGroupM = kGroupRows / (CG * BM);
-  const int per_group = kGroupM * p.tiles_n;
+// A unit of work: a tile, or one of `split` pieces of the reduction of one of the last tiles, which
+// would otherwise leave most SMs idle while they take a whole turn.
+struct Unit {
+  int tm, tn, k_lo, k_hi;
+};
+__device__ __forceinline__ int unit_count(const GemmParams& p) {
+  return p.whole + (p.tiles_m * p.tiles_n - p.whole) * p.split;
+}
+__device__ __forceinline__ Unit unit_of(const GemmParams& p, int u) {
+  Unit w;
+  int t = u;
+  w.k_lo = 0;
+  w.k_hi = p.nk;
+  if (u >= p.whole) {
+    const int v = u - p.whole, piece = v % p.split;
+    t = p.whole + v / p.split;
+    w.k_lo = static_cast<int>(static_cast<long long>(p.nk) * piece / p.split);
+    w.k_hi = static_cast<int>(static_cast<long long>(p.nk) * (piece + 1) / p.split);
+  }
+  const int per_group = p.group * p.tiles_n;
   const int g = t / per_group, in = t - g * per_group;
-  const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
-  tm = g * kGroupM + in % rows;
-  tn = in / rows;
+  const int rows = min(p.group, p.tiles_m - g * p.group);
+  w.tm = g * p.group + in % rows;
+  w.tn = in / rows;
+  return w;
 }
 
 // ---- many rows ------------------------------------------------------------------------------------
@@ -325,7 +356,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   pair_sync<CG>();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int tiles = p.tiles_m * p.tiles_n, first = blockIdx.x / CG, step = gridDim.x / CG;
+  const int units = unit_count(p), first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -334,14 +365,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t full0 = CG == 1 ? bar_full : in_cta(bar_full, 0);
       uint32_t g = 0;  // slices loaded so far
       int w = WAIT_OK;
-      for (int t = first; t < tiles && w == WAIT_OK; t += step) {
-        int tm, tn;
-        tile_of<CG>(p, t, tm, tn);
-        const int row0 = tm * CG * BM + static_cast<int>(rank) * BM, col0 = tn * TN + static_cast<int>(rank) * C::B_ROWS;
-        for (int k = 0; k < p.nk; ++k, ++g) {
+      for (int t = first; t < units && w == WAIT_OK; t += step) {
+        const Unit un = unit_of(p, t);
+        const int row0 = (un.tm * CG + static_cast<int>(rank)) * BM, col0 = un.tn * TN + static_cast<int>(rank) * C::B_ROWS;
+        for (int k = un.k_lo; k < un.k_hi; ++k, ++g) {
           const uint32_t s = g % C::NS;
           if (g >= C::NS) {
-            w = mbar_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort, kWaitLimitNs);
+            w = ring_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort);
             if (w != WAIT_OK) break;
           }
           // rank 1's bytes may land first: its slice is free, so the barrier is already in this phase
@@ -369,23 +399,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint64_t da0 = operand_desc<A_MN>(sb), db0 = operand_desc<B_MN>(sb + C::A_BYTES);
       uint32_t g = 0, it = 0;
       int w = WAIT_OK;
-      for (int t = first; t < tiles && w == WAIT_OK; t += step, ++it) {
+      for (int t = first; t < units && w == WAIT_OK; t += step, ++it) {
+        const Unit un = unit_of(p, t);
         const uint32_t acc = it & 1u;
         if (it >= 2) {
-          w = mbar_wait(bar_free + 8 * acc, (it / 2 - 1u) & 1u, s_abort, kWaitLimitNs);
+          w = ring_wait(bar_free + 8 * acc, (it / 2 - 1u) & 1u, s_abort);
           if (w != WAIT_OK) break;
           tc_fence_after();
         }
-        for (int k = 0; k < p.nk; ++k, ++g) {
+        for (int k = un.k_lo; k < un.k_hi; ++k, ++g) {
           const uint32_t s = g % C::NS;
-          w = mbar_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort, kWaitLimitNs);
+          w = ring_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort);
           if (w != WAIT_OK) break;
           tc_fence_after();
           const uint64_t da = da0 + ((s * C::STAGE) >> 4), db = db0 + ((s * C::STAGE) >> 4);
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
             pair_mma<CG>(tmem + acc * TN, da + kk * kDescStep<A_MN>, db + kk * kDescStep<B_MN>, idesc,
-                         (k > 0 || kk > 0) ? 1u : 0u);
+                         (k > un.k_lo || kk > 0) ? 1u : 0u);
           pair_commit<CG>(bar_empty + 8 * s);
         }
         if (w == WAIT_OK) pair_commit<CG>(bar_acc + 8 * acc);
@@ -403,9 +434,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t swz = (lane >> 1) & 3;  // 64-byte swizzle: 16-byte chunk c of row r sits at c ^ ((r / 2) % 4)
     const uint32_t free0 = CG == 1 ? bar_free : in_cta(bar_free, 0);
     uint32_t it = 0, stores = 0;
-    for (int t = first; t < tiles; t += step, ++it) {
-      int tm, tn;
-      tile_of<CG>(p, t, tm, tn);
+    for (int t = first; t < units; t += step, ++it) {
+      const Unit un = unit_of(p, t);
+      const int tm = un.tm, tn = un.tn;
       const uint32_t acc = it & 1u;
       const int row0 = (tm * CG + static_cast<int>(rank)) * BM + q * 32, row = row0 + lane;
       // the residual's values of a chunk of 32 columns are asked for one chunk ahead
@@ -420,7 +451,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       };
       ask(c_lo);
-      const int w = mbar_wait(bar_acc + 8 * acc, (it / 2) & 1u, s_abort, kWaitLimitNs);
+      const int w = ring_wait(bar_acc + 8 * acc, (it / 2) & 1u, s_abort);
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
       if (__any_sync(0xffffffffu, w != WAIT_OK)) break;
       tc_fence_after();
@@ -430,6 +461,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (col0 >= p.No) break;  // uniform: the rest of the tile is past the last column
         uint32_t r[32];
         tmem_ld_x32(tmem + lane_base + acc * TN + c, r);
+        if (t >= p.whole) {  // a piece: its sums as they are, 16 bytes per lane side by side, for the kernel that adds them
+          float4* to = reinterpret_cast<float4*>(p.part) +
+                       (((static_cast<size_t>(t - p.whole) * CG + rank) * 4 + q) * (TN / 32) + c / 32) * 256 + lane;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            to[32 * j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                                     __uint_as_float(r[4 * j + 3]));
+          continue;
+        }
         f2 v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
@@ -503,6 +543,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (warp == 1) pair_tmem_dealloc<CG>(tmem, C::TMEM_COLS);
 }
 
+// The pieces of the last tiles added, in order, and rounded: one warp per 32 x 32 outputs. Only products
+// without an epilogue (the gradients) are split.
+template <int CG, int TN>
+__global__ void __launch_bounds__(256) sol_linear_pieces_kernel(const __grid_constant__ GemmParams p, __nv_bfloat16* out) {
+  const int lane = threadIdx.x & 31, i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  constexpr int kChunks = CG * 4 * (TN / 32);
+  const int tile = i / kChunks, in = i - tile * kChunks;
+  if (tile >= p.tiles_m * p.tiles_n - p.whole) return;
+  const Unit un = unit_of(p, p.whole + tile * p.split);
+  const int row = un.tm * CG * BM + in / (TN / 32) * 32 + lane, col0 = un.tn * TN + in % (TN / 32) * 32;
+  float4 s[8];
+  const float4* from = reinterpret_cast<const float4*>(p.part) + (static_cast<size_t>(tile) * p.split * kChunks + in) * 256 + lane;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = __ldcs(from + 32 * j);
+  for (int piece = 1; piece < p.split; ++piece) {
+    from += static_cast<size_t>(kChunks) * 256;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 a = __ldcs(from + 32 * j);
+      s[j].x += a.x;
+      s[j].y += a.y;
+      s[j].z += a.z;
+      s[j].w += a.w;
+    }
+  }
+  if (row >= p.Mo) return;
+  __nv_bfloat16* o = out + static_cast<size_t>(row) * p.No + col0;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2)
+    if (col0 + 4 * j < p.No)
+      *reinterpret_cast<uint4*>(o + 4 * j) = make_uint4(pack_bf16x2(s[j].x, s[j].y), pack_bf16x2(s[j].z, s[j].w),
+                                                        pack_bf16x2(s[j + 1].x, s[j + 1].y), pack_bf16x2(s[j + 1].z, s[j + 1].w));
+}
+
 // ---- few rows --------------------------------------------------------------------------------------
 constexpr int kFewThreads = 192;
 
@@ -574,7 +648,7 @@ __global__ void __launch_bounds__(kFewThreads)
       for (int k = k_lo; k < k_hi; ++k, ++g) {
         const uint32_t s = g % C::NS;
         if (g >= C::NS) {
-          w = mbar_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort, kWaitLimitNs);
+          w = ring_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort);
           if (w != WAIT_OK) break;
         }
         mbar_arrive_expect_tx(bar_full + 8 * s, C::STAGE);
@@ -594,7 +668,7 @@ __global__ void __launch_bounds__(kFewThreads)
       int w = WAIT_OK;
       for (int k = k_lo; k < k_hi; ++k, ++g) {
         const uint32_t s = g % C::NS;
-        w = mbar_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort, kWaitLimitNs);
+        w = ring_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort);
         if (w != WAIT_OK) break;
         tc_fence_after();
         const uint64_t da = da0 + ((s * C::STAGE) >> 4), db = db0 + ((s * C::STAGE) >> 4);
@@ -609,7 +683,7 @@ __global__ void __launch_bounds__(kFewThreads)
     }
     __syncwarp();
   } else {
-    const int w = mbar_wait(bar_acc, 0, nullptr, 2 * kWaitLimitNs);
+    const int w = ring_wait(bar_acc, 0, nullptr);
     if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
     ok = !__any_sync(0xffffffffu, w != WAIT_OK);
     if (ok) {
@@ -762,8 +836,15 @@ cudaError_t launch_gemm_t(const GemmArgs& a, GemmParams p, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   const int units = a.num_sms / CG;
+  const double rows = kGroupBytes / (2.0 * a.Ko);
+  p.group = static_cast<int>(rows > kGroupRows ? rows < 1e6 ? rows : 1e6 : kGroupRows) / (CG * BM);
+  if (p.group > p.tiles_m) p.group = p.tiles_m;
+  const int rest = static_cast<int>(tiles % units);
+  p.split = a.tile.split;
+  p.whole = static_cast<int>(tiles) - (p.split > 1 ? rest : 0);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CG * static_cast<int>(tiles < units ? tiles : units));
+  const long long work = p.whole + static_cast<long long>(rest) * (p.split > 1 ? p.split : 0);
+  cfg.gridDim = dim3(CG * static_cast<int>(work < units ? work : units));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
@@ -774,7 +855,11 @@ cudaError_t launch_gemm_t(const GemmArgs& a, GemmParams p, cudaStream_t stream) 
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, sol_linear_kernel<CG, TN, A_MN, B_MN>, a.maps[0], a.maps[1], a.maps[2], a.maps[3], p);
+  const cudaError_t le = cudaLaunchKernelEx(&cfg, sol_linear_kernel<CG, TN, A_MN, B_MN>, a.maps[0], a.maps[1], a.maps[2],
+                                            a.maps[3], p);
+  if (le != cudaSuccess || p.split == 1) return le;
+  sol_linear_pieces_kernel<CG, TN><<<rest * CG * 4 * (TN / 32) / 8, 256, 0, stream>>>(p, static_cast<__nv_bfloat16*>(a.out));
+  return cudaGetLastError();
 }
 
 template <bool A_MN, bool B_MN>
@@ -806,22 +891,33 @@ cudaError_t launch_few_t(const FewArgs& a, const FewParams& p, cudaStream_t stre
 
 }  // namespace
 
-GemmTile linear_tile(int Mo, int No, int num_sms) {
-  // time of the last SM to finish, in columns of a 256 x 256 pair tile's rate: a smaller tile re-reads more
-  // operand bytes per product and runs at a lower rate
-  const struct { GemmTile tile; double cost; } options[] = {{{2, 256}, 256.0}, {{2, 128}, 150.0}, {{1, 128}, 160.0}, {{1, 64}, 105.0}};
-  GemmTile best = options[0].tile;
+GemmTile linear_tile(int Mo, int No, int Ko, bool splittable, int num_sms) {
+  // SM cycles until the last one is done, from measured products: a slice (64 deep) takes about as long on
+  // the smaller tiles, which wait for their operands, as the 512 MMA cycles of the largest; the last
+  // epilogue is not overlapped. (8191 x 768 -> 768 takes 15.2, 18.9, 18.1 and 28.7 us in this order,
+  // 1000 x 768 -> 768 10.5, 10.2, 8.6 and 8.0 us.)
+  const struct { int ctas, n; double slice, last; } options[] = {
+      {2, 256, 600.0, 6500.0}, {2, 128, 510.0, 6000.0}, {1, 128, 545.0, 4000.0}, {1, 64, 487.0, 3200.0}};
+  const int nk = (Ko + BK - 1) / BK;
+  GemmTile best = {};
   double least = 0.0;
   for (const auto& o : options) {
-    const double tiles = std::ceil(Mo / (128.0 * o.tile.ctas)) * std::ceil(No / static_cast<double>(o.tile.n));
-    const double t = std::ceil(tiles / (num_sms / o.tile.ctas)) * o.cost;
-    if (least == 0.0 || t < least) {
-      least = t;
-      best = o.tile;
+    const int units = num_sms / o.ctas;
+    const long long tiles = static_cast<long long>(std::ceil(Mo / (128.0 * o.ctas))) * ((No + o.n - 1) / o.n);
+    const int rest = static_cast<int>(tiles % units);
+    for (int split = 1; split == 1 || (splittable && rest > 0 && rest * split <= units && nk / split >= kPieceSlices); ++split) {
+      const double turns = static_cast<double>(tiles / units) * nk + (rest > 0 ? std::ceil(nk / static_cast<double>(split)) : 0.0);
+      const double t = turns * o.slice + o.last + (split > 1 ? kPieceCycles : 0.0);
+      if (least == 0.0 || t < least) {
+        least = t;
+        best = {o.ctas, o.n, split};
+      }
     }
   }
   return best;
 }
+
+size_t linear_part_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 128 * 256 * 4; }
 
 int linear_few_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
@@ -842,6 +938,7 @@ cudaError_t launch_linear_gemm(const GemmArgs& a, cudaStream_t stream) {
   p.residual = static_cast<const __nv_bfloat16*>(a.residual);
   p.act = a.act;
   p.store_z = a.store_z;
+  p.part = a.part;
   p.ws = a.ws;
   if (a.a_mn) return launch_gemm_n<true, true>(a, p, stream);
   return a.b_mn ? launch_gemm_n<false, true>(a, p, stream) : launch_gemm_n<false, false>(a, p, stream);
