@@ -122,7 +122,11 @@ sol_status run_gemm(sol::GemmArgs& a, const void* A, const void* Bm, void* out, 
   if ((st = make_operand_map(&a.maps[0], A, a.a_mn ? a.Ko : a.Mo, a.a_mn ? a.Mo : a.Ko, a.a_mn, 128)) != SOL_OK) return st;
   if ((st = make_operand_map(&a.maps[1], Bm, a.b_mn ? a.Ko : a.No, a.b_mn ? a.No : a.Ko, a.b_mn, a.tile.n / a.tile.ctas)) != SOL_OK) return st;
   if ((st = make_map2d(&a.maps[2], out, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK) return st;
-  if ((st = make_map2d(&a.maps[3], z != nullptr ? z : out, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK) return st;
+  a.maps[3] = a.maps[4] = a.maps[2];
+  if (z != nullptr && (st = make_map2d(&a.maps[3], z, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK) return st;
+  if (a.residual != nullptr &&
+      (st = make_map2d(&a.maps[4], a.residual, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK)
+    return st;
   const cudaError_t e = sol::launch_linear_gemm(a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "linear layer launch");
   return SOL_OK;

@@ -199,7 +199,7 @@ size_t linear_part_bytes(int num_sms);           // accumulators of one tile per
 int linear_few_tile(int M);                      // tokens per tile of the kernel for few rows
 int linear_dz_chunks(int M, int N);              // row blocks of the dz pass, one partial column sum each
 struct GemmArgs {
-  CUtensorMap maps[4];  // A, B (boxes as launch_linear_gemm's tiles want them), out, z
+  CUtensorMap maps[5];  // A, B (boxes as launch_linear_gemm's tiles want them), out, z, residual
   int Mo, No, Ko;       // output rows, columns, reduction
   bool a_mn, b_mn;      // operand is MN-major: its memory rows run along M or N
   GemmTile tile;

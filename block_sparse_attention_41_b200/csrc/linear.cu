@@ -63,7 +63,7 @@ struct GemmCfg {
   static constexpr int NS = 196608 / STAGE;  // 6 or 8 slices of 32 or 24 KB
   static constexpr int OFF_EPI = NS * STAGE;
   static constexpr int OFF_BAR = OFF_EPI + kEpiWarps * 2 * kEpiBuf;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // + alignment of the ring to 1024 bytes
+  static constexpr int SMEM = OFF_BAR + 384 + 1024;  // + alignment of the ring to 1024 bytes
   static constexpr int TMEM_COLS = 2 * TN;
 };
 
@@ -74,9 +74,8 @@ struct GemmParams {
   int whole, split;      // units from `whole` on are pieces of the last tiles, `split` of each
   float* part;           // their fp32 accumulators, or null
   const float* bias;               // [No] or null
-  const __nv_bfloat16* residual;   // [Mo, No] or null
   int act;
-  int store_z;
+  int has_residual, store_z;
   uint32_t* ws;  // error words, or null
 };
 
@@ -323,6 +322,7 @@ template <int CG, int TN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     sol_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
+                      const __grid_constant__ CUtensorMap map_res,
                       const __grid_constant__ GemmParams p) {
   using C = GemmCfg<CG, TN>;
   extern __shared__ uint8_t smem_raw[];
@@ -331,9 +331,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* smem = smem_raw + (sb - raw);
   const uint32_t bars = sb + C::OFF_BAR;
   const uint32_t bar_full = bars, bar_empty = bars + 8 * C::NS, bar_acc = bars + 16 * C::NS,
-                 bar_free = bar_acc + 16, bar_drain = bar_free + 16;
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 16 * C::NS + 40);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 16 * C::NS + 44);
+                 bar_free = bar_acc + 16, bar_drain = bar_free + 16, bar_res = bar_drain + 8;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 16 * C::NS + 40 + 16 * kEpiWarps);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 16 * C::NS + 44 + 16 * kEpiWarps);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 1 ? 0u : cluster_rank();  // rank 0 issues the MMAs of a pair
@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(bar_free + 8 * a, CG * kEpiWarps);  // of a pair only rank 0's
     }
     mbar_init(bar_drain, 1);
+    for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(bar_res + 8 * i, 1);
     fence_mbar_init();
     *s_abort = 0;
   }
@@ -433,27 +434,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t buf0 = sb + C::OFF_EPI + ew * 2 * kEpiBuf;
     const uint32_t swz = (lane >> 1) & 3;  // 64-byte swizzle: 16-byte chunk c of row r sits at c ^ ((r / 2) % 4)
     const uint32_t free0 = CG == 1 ? bar_free : in_cta(bar_free, 0);
-    uint32_t it = 0, stores = 0;
+    const uint32_t bar_mine = bar_res + 16 * ew;
+    uint32_t it = 0, chunks = 0, asked = 0;  // chunks stored; residual chunks asked for
     for (int t = first; t < units; t += step, ++it) {
       const Unit un = unit_of(p, t);
       const int tm = un.tm, tn = un.tn;
       const uint32_t acc = it & 1u;
-      const int row0 = (tm * CG + static_cast<int>(rank)) * BM + q * 32, row = row0 + lane;
-      // the residual's values of a chunk of 32 columns are asked for one chunk ahead
-      const bool live = p.residual != nullptr && row < p.Mo;
-      const __nv_bfloat16* res = p.residual + static_cast<size_t>(row) * p.No + tn * TN;
-      uint4 ahead[4];
-      auto ask = [&](int c) {
-        if (live && c < c_lo + TN / 2) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (tn * TN + c + 8 * i < p.No) ahead[i] = __ldg(reinterpret_cast<const uint4*>(res + c + 8 * i));
+      const int row0 = (tm * CG + static_cast<int>(rank)) * BM + q * 32;
+      // The residual's values of a chunk come by TMA, one chunk ahead, into the buffer from which the chunk
+      // will be stored: rows read by their own lanes (16 bytes of 32 rows at a time) held the whole
+      // epilogue back.
+      auto ask = [&](int col, int pending) {  // pending: stores after the last one out of this buffer
+        const uint32_t i = asked & 1u;
+        if (lane == 0) {
+          if (pending == 0) bulk_wait_read<0>();
+          else bulk_wait_read<1>();
+          mbar_arrive_expect_tx(bar_mine + 8 * i, kEpiBuf);
+          tma_load_2d(buf0 + i * kEpiBuf, &map_res, bar_mine + 8 * i, col, row0);
         }
+        ++asked;
       };
-      ask(c_lo);
+      const bool with_res = p.has_residual;  // past the last row too: zeros, so that every chunk counts alike
+      if (with_res && tn * TN + c_lo < p.No) ask(tn * TN + c_lo, 1);
+      float4 bias[8];  // of a chunk, read ahead as well
+      auto read_bias = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // No is a multiple of 8
+          if (c < c_lo + TN / 2 && tn * TN + c + 4 * j < p.No)
+            bias[j] = __ldg(reinterpret_cast<const float4*>(p.bias + tn * TN + c + 4 * j));
+      };
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bias[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.bias != nullptr) read_bias(c_lo);
       const int w = ring_wait(bar_acc + 8 * acc, (it / 2) & 1u, s_abort);
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
-      if (__any_sync(0xffffffffu, w != WAIT_OK)) break;
+      if (__any_sync(0xffffffffu, w != WAIT_OK)) {
+        // a copy of the residual's must not outlive the buffer
+        if (asked != chunks && with_res) mbar_wait(bar_mine + 8 * (chunks & 1u), (chunks >> 1) & 1u, nullptr, kWaitLimitNs);
+        break;
+      }
       tc_fence_after();
 #pragma unroll 1
       for (int c = c_lo; c < c_lo + TN / 2; c += 32) {
@@ -473,9 +492,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         f2 v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        const uint32_t buf = buf0 + (chunks & 1u) * kEpiBuf;
+        bool fresh = true;  // nothing of this chunk has left through its buffer yet
         auto emit = [&](const CUtensorMap* map) {
-          const uint32_t buf = buf0 + (stores & 1u) * kEpiBuf;
-          if (lane == 0) bulk_wait_read<1>();  // the store before the last one has left this buffer
+          if (lane == 0) {
+            if (!fresh) bulk_wait_read<0>();
+            else if (!with_res) bulk_wait_read<1>();  // the store before the last one has left this buffer
+          }
+          fresh = false;
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -495,36 +519,44 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (row0 < p.Mo) tma_store_2d(map, buf, col0, row0);  // rows and columns past the end are not written
             bulk_commit();
           }
-          ++stores;
         };
         if (p.bias != nullptr) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            if (col0 + 4 * j < p.No) {  // No is a multiple of 8
-              const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col0 + 4 * j));
-              v[2 * j] = add2(v[2 * j], pack2(b.x, b.y));
-              v[2 * j + 1] = add2(v[2 * j + 1], pack2(b.z, b.w));
-            }
+            v[2 * j] = add2(v[2 * j], pack2(bias[j].x, bias[j].y));
+            v[2 * j + 1] = add2(v[2 * j + 1], pack2(bias[j].z, bias[j].w));
           }
+          read_bias(c + 32);
+        }
+        uint4 res[4];
+        if (with_res) {
+          if (c + 32 < c_lo + TN / 2 && col0 + 32 < p.No) ask(col0 + 32, 0);
+          const uint32_t i = chunks & 1u;
+          const int rw = ring_wait(bar_mine + 8 * i, (chunks >> 1) & 1u, s_abort);
+          if (rw == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(res[j].x), "=r"(res[j].y), "=r"(res[j].z), "=r"(res[j].w)
+                         : "r"(buf + lane * 64 + ((j ^ swz) << 4))
+                         : "memory");
         }
         if (p.store_z) emit(&map_z);
         with_activation(p.act, [&](auto kind) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = activate<decltype(kind)::value>(v[j]);
         });
-        if (live) {
+        if (with_res) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (col0 + 8 * i < p.No) {
-              const uint32_t wv[4] = {ahead[i].x, ahead[i].y, ahead[i].z, ahead[i].w};
+            const uint32_t wv[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[4 * i + j] = add2(v[4 * i + j], pack2(__uint_as_float(wv[j] << 16), __uint_as_float(wv[j] & 0xffff0000u)));
-            }
+            for (int j = 0; j < 4; ++j)
+              v[4 * i + j] = add2(v[4 * i + j], pack2(__uint_as_float(wv[j] << 16), __uint_as_float(wv[j] & 0xffff0000u)));
           }
         }
-        ask(c + 32);
         emit(&map_out);
+        ++chunks;
       }
       tc_fence_before();
       __syncwarp();
@@ -856,7 +888,7 @@ cudaError_t launch_gemm_t(const GemmArgs& a, GemmParams p, cudaStream_t stream) 
   cfg.attrs = attr;
   cfg.numAttrs = CG > 1 ? 1 : 0;
   const cudaError_t le = cudaLaunchKernelEx(&cfg, sol_linear_kernel<CG, TN, A_MN, B_MN>, a.maps[0], a.maps[1], a.maps[2],
-                                            a.maps[3], p);
+                                            a.maps[3], a.maps[4], p);
   if (le != cudaSuccess || p.split == 1) return le;
   sol_linear_pieces_kernel<CG, TN><<<rest * CG * 4 * (TN / 32) / 8, 256, 0, stream>>>(p, static_cast<__nv_bfloat16*>(a.out));
   return cudaGetLastError();
@@ -935,7 +967,7 @@ cudaError_t launch_linear_gemm(const GemmArgs& a, cudaStream_t stream) {
   p.No = a.No;
   p.nk = (a.Ko + BK - 1) / BK;
   p.bias = a.bias;
-  p.residual = static_cast<const __nv_bfloat16*>(a.residual);
+  p.has_residual = a.residual != nullptr;
   p.act = a.act;
   p.store_z = a.store_z;
   p.part = a.part;
