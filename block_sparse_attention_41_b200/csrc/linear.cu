@@ -193,14 +193,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank) {
   uint32_t a;
-  float v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
-
 // The address of this CTA's shared memory `addr` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   uint32_t a;
@@ -617,7 +616,7 @@ struct FewCfg {
   static constexpr int A_BYTES = BM * BK * 2;  // 128 rows of w
   static constexpr int B_BYTES = TT * BK * 2;  // TT tokens
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int NS = 6;
+  static constexpr int NS = 3;  // few, so that several CTAs share an SM and one loads while another finishes
   static constexpr int PART = TT * BM * 4;     // fp32 partial tile [token][row of w], over the ring once it is done
   static constexpr int RING = NS * STAGE > PART ? NS * STAGE : PART;
   static constexpr int OFF_BAR = RING;
@@ -739,24 +738,47 @@ __global__ void __launch_bounds__(kFewThreads)
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
   const bool aborted = *s_abort != 0;
   if (p.split > 1) cluster_arrive_wait();
-  // each CTA of the cluster finishes an equal share of the M x 128 values (128 is a multiple of split)
+  // each CTA of the cluster finishes an equal share of the M x 128 values, four at a time (128 / 4 is a
+  // multiple of split)
   if (!aborted) {
-    const int share = p.M * BM / p.split;
+    const int share = p.M * (BM / 4) / p.split;
     for (int e = rank * share + tid; e < (rank + 1) * share; e += kFewThreads) {
-      const int m = e / BM, n = n0 + (e & (BM - 1));
-      float v = 0.f;
+      const int m = e / (BM / 4), n = n0 + 4 * (e & (BM / 4 - 1));
+      if (n >= p.N) continue;  // N is a multiple of 8
+      f2 v[2];
       if (p.split == 1) {
-        v = reinterpret_cast<const float*>(smem)[e];
+        const float4 f = reinterpret_cast<const float4*>(smem)[e];
+        v[0] = pack2(f.x, f.y);
+        v[1] = pack2(f.z, f.w);
       } else {
-        for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(sb + 4 * e, r);
+        v[0] = v[1] = dup2(0.f);
+        for (int r = 0; r < p.split; ++r) {
+          const float4 f = ld_cluster_f32x4(sb + 16 * e, r);
+          v[0] = add2(v[0], pack2(f.x, f.y));
+          v[1] = add2(v[1], pack2(f.z, f.w));
+        }
       }
-      if (n >= p.N) continue;
-      if (p.bias != nullptr) v += __ldg(p.bias + n);
+      if (p.bias != nullptr) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(p.bias + n));
+        v[0] = add2(v[0], pack2(f.x, f.y));
+        v[1] = add2(v[1], pack2(f.z, f.w));
+      }
       const size_t o = static_cast<size_t>(m) * p.N + n;
-      if (p.z != nullptr) p.z[o] = __float2bfloat16_rn(v);
-      with_activation(p.act, [&](auto kind) { v = unpack2(activate<decltype(kind)::value>(dup2(v))).x; });
-      if (p.residual != nullptr) v += __bfloat162float(p.residual[o]);
-      p.out[o] = __float2bfloat16_rn(v);
+      auto put = [&](__nv_bfloat16* to) {
+        const float2 lo = unpack2(v[0]), hi = unpack2(v[1]);
+        *reinterpret_cast<uint2*>(to + o) = make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(hi.x, hi.y));
+      };
+      if (p.z != nullptr) put(p.z);
+      with_activation(p.act, [&](auto kind) {
+        v[0] = activate<decltype(kind)::value>(v[0]);
+        v[1] = activate<decltype(kind)::value>(v[1]);
+      });
+      if (p.residual != nullptr) {
+        const uint2 r = *reinterpret_cast<const uint2*>(p.residual + o);
+        v[0] = add2(v[0], pack2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u)));
+        v[1] = add2(v[1], pack2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u)));
+      }
+      put(p.out);
     }
   }
   if (p.split > 1) cluster_arrive_wait();  // no CTA leaves while another reads its partial tile
@@ -987,10 +1009,12 @@ cudaError_t launch_linear_few(const FewArgs& a, cudaStream_t stream) {
   p.z = static_cast<__nv_bfloat16*>(a.z);
   p.act = a.act;
   p.ws = a.ws;
-  // the reduction over 1, 2, 4 or 8 CTAs: until there are four CTAs per SM, as long as each keeps 8 slices
+  // the reduction over 1, 2, 4 or 8 CTAs: as many as are resident at once, each with two slices at least
+  // (2 x 5120 -> 30720: 49.7 us over 2, 52.2 over 4; 16 x 4096 -> 4096: 17.3, 12.2 and 11.0 over 2, 4, 8)
+  const int resident = a.num_sms * (a.M <= 16 ? 4 : a.M <= 64 ? 3 : 2);
   const int tiles = (a.N + BM - 1) / BM;
   p.split = 1;
-  while (p.split < 8 && tiles * p.split < 4 * a.num_sms && p.nk / (2 * p.split) >= 8) p.split *= 2;
+  while (p.split < 8 && tiles * 2 * p.split <= resident && p.nk / (2 * p.split) >= 2) p.split *= 2;
   switch (linear_few_tile(a.M)) {
     case 16: return launch_few_t<16>(a, p, stream);
     case 32: return launch_few_t<32>(a, p, stream);
