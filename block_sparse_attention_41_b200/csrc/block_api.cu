@@ -285,7 +285,7 @@ sol_status sol_attn_rope_tables(const int32_t* pos, int axes, const int* section
   a.factor = attn_factor;
   a.cos = rope_cos;
   a.sin = rope_sin;
-  const cudaError_t e = sol::launch_rope_tables(a, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = sol::launch_rope_tables(a, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rotary table launch");
   return SOL_OK;
 }

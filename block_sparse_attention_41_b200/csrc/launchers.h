@@ -184,7 +184,7 @@ struct RopeTableArgs {
   float* cos;  // [L, rot / 2]
   float* sin;
 };
-cudaError_t launch_rope_tables(const RopeTableArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_tables(const RopeTableArgs& a, int num_sms, cudaStream_t stream);
 
 // Linear layer (sol_attn_linear) and its gradients: bf16 operands, fp32 accumulation.
 enum : int { ACT_NONE = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_SILU = 3 };

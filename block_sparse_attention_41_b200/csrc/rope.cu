@@ -5,9 +5,11 @@
 // with m the factor of a stretched context; the inverse turns by -angle (the gradient of the first).
 // Pairs are interleaved, (2i, 2i + 1), or halves, (i, i + rot / 2); channels from rot on pass through.
 //
-// Angles are formed in 64 bits: a position of 10^6 turns its fastest pair by 10^6 radians, where a
-// 32-bit angle is off by 0.03. The angle over pi is reduced to [-1, 1] there and only the rest goes
-// to 32 bits, so cosine and sine are good to about 2e-7 at every position.
+// A position of 10^6 turns its fastest pair by 10^6 radians, where a 32-bit angle is off by 0.03. So a
+// pair's turn per position, modulo one, becomes a 64-bit fraction, and the angle is position times
+// fraction in integers, where whole turns fall off by themselves; its top 32 bits are the angle to
+// 2^-32 of a turn. Cosine and sine of what is left of it in the nearest quarter turn come from their
+// Taylor series, good to about 1e-7 at every position. The 64-bit float work is one product per pair.
 //
 // HBM-bound: every element is read and written once. A thread owns one 16-byte vector of columns (a
 // vector of each half in the half layout) of one token, forms its cosines and sines once and then
@@ -24,16 +26,37 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// m cos, m sin of pair i at the given token (column of pos)
-__device__ __forceinline__ void turn(const int* pos, int L, const double* inv_freq, const int (&end)[4], int i,
-                                     float factor, float& c, float& s) {
-  const int axis = (i >= end[0]) + (i >= end[1]) + (i >= end[2]);
-  const double x = static_cast<double>(__ldg(pos + static_cast<size_t>(axis) * L)) * __ldg(inv_freq + i) *
-                   0.31830988618379067154;  // angle / pi
-  const double y = x - 2.0 * rint(0.5 * x);
-  sincospif(static_cast<float>(y), &s, &c);
-  c *= factor;
-  s *= factor;
+// Turn per position of a pair, modulo one, as a 64-bit fraction.
+__device__ __forceinline__ unsigned long long turn_fraction(double inv_freq) {
+  const double f = inv_freq * 0.15915494309189533577;  // over 2 pi
+  return __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
+}
+// m cos, m sin at a position.
+__device__ __forceinline__ void turn(int pos, unsigned long long fraction, float m, float& c, float& s) {
+  const uint32_t lo = static_cast<uint32_t>(fraction), hi = static_cast<uint32_t>(fraction >> 32);
+  uint32_t a = static_cast<uint32_t>(pos) * hi + __umulhi(static_cast<uint32_t>(pos), lo);
+  if (pos < 0) a -= lo;  // the product of a negative position, as its low 32 bits are above 0
+  const uint32_t quarter = (a + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int>(a - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi 2^-32: |x| <= pi / 4
+  const float q = x * x;
+  // degrees 9 and 10: the next terms are below 2e-9 and 2e-10 of the first
+  float sn = fmaf(q, 2.7557319e-6f, -1.9841270e-4f);
+  sn = fmaf(sn, q, 8.3333333e-3f);
+  sn = fmaf(sn, q, -1.6666667e-1f);
+  sn = fmaf(sn * q, x, x);
+  float cs = fmaf(q, -2.7557319e-7f, 2.4801587e-5f);
+  cs = fmaf(cs, q, -1.3888889e-3f);
+  cs = fmaf(cs, q, 4.1666667e-2f);
+  cs = fmaf(cs, q, -0.5f);
+  cs = fmaf(cs, q, 1.0f);
+  const float cc = (quarter & 1u) ? sn : cs, ss = (quarter & 1u) ? cs : sn;  // cos(x + pi/2) = -sin x, ..
+  c = ((quarter + 1u) & 2u) ? -m * cc : m * cc;
+  s = (quarter & 2u) ? -m * ss : m * ss;
+}
+__device__ __forceinline__ int axis_of(const int (&end)[4], int i) { return (i >= end[0]) + (i >= end[1]) + (i >= end[2]); }
+__device__ __forceinline__ void turn_of(const RopeArgs& p, int b, int t, int i, float& c, float& s) {
+  turn(__ldg(p.pos + b * p.pos_b + static_cast<size_t>(axis_of(p.end, i)) * p.L + t), turn_fraction(__ldg(p.inv_freq + i)),
+       p.factor, c, s);
 }
 
 template <typename T, int V>
@@ -121,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) sol_rope_interleaved_kernel(const __
   for (int k = 0; k < V / 2; ++k) {
     c[k] = 1.f;
     s[k] = 0.f;
-    if (2 * k < turned) turn(p.pos + b * p.pos_b + t, p.L, p.inv_freq, p.end, col / 2 + k, p.factor, c[k], s[k]);
+    if (2 * k < turned) turn_of(p, b, t, col / 2 + k, c[k], s[k]);
     if (p.inverse) s[k] = -s[k];
   }
   for_heads<T>(p, b, t, h0, h1, [&](const T* in, T* out, long long ih, long long oh, int lo, int hi) {
@@ -171,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) sol_rope_half_kernel(const __grid_co
   float c[V], s[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    turn(p.pos + b * p.pos_b + t, p.L, p.inv_freq, p.end, col + k, p.factor, c[k], s[k]);
+    turn_of(p, b, t, col + k, c[k], s[k]);
     if (p.inverse) s[k] = -s[k];
   }
   for_heads<T>(p, b, t, h0, h1, [&](const T* in, T* out, long long ih, long long oh, int lo, int hi) {
@@ -212,16 +235,35 @@ cudaError_t launch_t(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-__global__ void __launch_bounds__(kThreads) sol_rope_tables_kernel(const __grid_constant__ RopeTableArgs p) {
-  const int half = p.rot / 2;
-  const long long n = static_cast<long long>(p.L) * half;
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= n) return;
-  const int t = static_cast<int>(i / half), j = static_cast<int>(i - static_cast<long long>(t) * half);
-  float c, s;
-  turn(p.pos + t, p.L, p.inv_freq, p.end, j, p.factor, c, s);
-  p.cos[i] = c;
-  p.sin[i] = s;
+// Tables: V pairs of one token per thread and turn of the loop, the same pairs every time, so that
+// their fractions stay in registers. Bound by the stores.
+template <int V>
+__global__ void __launch_bounds__(kThreads) sol_rope_tables_kernel(const __grid_constant__ RopeTableArgs p, int groups, int tokens) {
+  const int half = p.rot / 2, g = threadIdx.x % groups;
+  if (threadIdx.x >= groups * tokens) return;
+  for (int j = g * V; j < half; j += groups * V) {
+    unsigned long long f[V];
+    const int* pos[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      f[k] = turn_fraction(__ldg(p.inv_freq + j + k));
+      pos[k] = p.pos + static_cast<size_t>(axis_of(p.end, j + k)) * p.L;
+    }
+    const long long step = static_cast<long long>(gridDim.x) * tokens;
+    for (long long t = static_cast<long long>(blockIdx.x) * tokens + threadIdx.x / groups; t < p.L; t += step) {
+      float c[V], s[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) turn(__ldg(pos[k] + t), f[k], p.factor, c[k], s[k]);
+      const size_t o = static_cast<size_t>(t) * half + j;
+      if constexpr (V == 4) {
+        *reinterpret_cast<float4*>(p.cos + o) = make_float4(c[0], c[1], c[2], c[3]);
+        *reinterpret_cast<float4*>(p.sin + o) = make_float4(s[0], s[1], s[2], s[3]);
+      } else {
+        p.cos[o] = c[0];
+        p.sin[o] = s[0];
+      }
+    }
+  }
 }
 
 }  // namespace
@@ -231,9 +273,14 @@ cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   return a.vec ? launch_t<float, 4>(a, num_sms, stream) : launch_t<float, 1>(a, num_sms, stream);
 }
 
-cudaError_t launch_rope_tables(const RopeTableArgs& a, cudaStream_t stream) {
-  const long long n = static_cast<long long>(a.L) * (a.rot / 2);
-  sol_rope_tables_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+cudaError_t launch_rope_tables(const RopeTableArgs& a, int num_sms, cudaStream_t stream) {
+  const int half = a.rot / 2;
+  const bool vec = half % 4 == 0 && (reinterpret_cast<uintptr_t>(a.cos) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.sin) & 15u) == 0;
+  const int per_token = vec ? half / 4 : half, groups = per_token < kThreads ? per_token : kThreads, tokens = kThreads / groups;
+  const long long blocks = (static_cast<long long>(a.L) + tokens - 1) / tokens, most = 8ll * num_sms;
+  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+  if (vec) sol_rope_tables_kernel<4><<<grid, kThreads, 0, stream>>>(a, groups, tokens);
+  else sol_rope_tables_kernel<1><<<grid, kThreads, 0, stream>>>(a, groups, tokens);
   return cudaGetLastError();
 }
 
