@@ -85,6 +85,7 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
 template <typename T, int V, int E, bool FULL>
 struct Lane {
   static constexpr int NV = E / V, P = E / 2;
+  static constexpr bool kFull = FULL;
   int tpr, t, C;
   uint32_t smem, step;
 
@@ -200,11 +201,12 @@ __device__ __forceinline__ RowGroup row_group(float* s_buf, int tpr) {
 
 // Sums of N values over a row, the same for all its threads. Each thread adds the warps' sums itself:
 // a few 16-byte broadcasts take a third of the latency of five more shuffles.
-template <int N>
+// WARPS: a row has whole warps.
+template <bool WARPS, int N>
 __device__ __forceinline__ void row_sum(RowGroup& g, float (&v)[N]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    if (o < g.width) {
+    if (WARPS || o < g.width) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
@@ -239,7 +241,7 @@ __device__ __forceinline__ float centre(const L& l, RowGroup& g, f2 (&x)[L::P], 
 #pragma unroll
     for (int i = 1; i < L::P; ++i) s = add2(s, x[i]);
     float v[1] = {sum2(s)};
-    row_sum(g, v);
+    row_sum<L::kFull>(g, v);
     const f2 m = pack2(-v[0] * inv_c, -v[0] * inv_c);
 #pragma unroll
     for (int i = 0; i < L::P; ++i) x[i] = add2(x[i], m);
@@ -249,7 +251,7 @@ __device__ __forceinline__ float centre(const L& l, RowGroup& g, f2 (&x)[L::P], 
 #pragma unroll
   for (int i = 1; i < L::P; ++i) q = fma2(x[i], x[i], q);
   float v[1] = {sum2(q)};
-  row_sum(g, v);
+  row_sum<L::kFull>(g, v);
   return 1.0f / sqrtf(fmaf(v[0], inv_c, eps));
 }
 template <int P>
@@ -274,12 +276,12 @@ __device__ __forceinline__ void normalise_back(const L& l, RowGroup& g, f2 (&w)[
 #pragma unroll
     for (int i = 1; i < L::P; ++i) m = add2(m, w[i]);
     float v[2] = {sum2(s), sum2(m)};
-    row_sum(g, v);
+    row_sum<L::kFull>(g, v);
     a = -v[0] * inv_c * r;
     m = pack2(-v[1] * inv_c, -v[1] * inv_c);
   } else {
     float v[1] = {sum2(s)};
-    row_sum(g, v);
+    row_sum<L::kFull>(g, v);
     a = -v[0] * inv_c * r;
   }
   const f2 rr = pack2(r, r), aa = pack2(a, a);
@@ -575,14 +577,14 @@ __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const
   }
 }
 
-constexpr int kSumCols = 32, kSumRows = 16;
+constexpr int kSumCols = 32, kSumRows = 32;
 
 // Sums over `n` rows of one column, by the kSumRows threads of a block column; all of them return it.
 template <typename F>
 __device__ __forceinline__ float column_sum(F&& get, int n) {
   __shared__ float s[kSumRows][kSumCols + 1];
   float a = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = threadIdx.y; i < n; i += kSumRows) a += get(i);
   __syncthreads();
   s[threadIdx.y][threadIdx.x] = a;
@@ -593,42 +595,33 @@ __device__ __forceinline__ float column_sum(F&& get, int n) {
   return t;
 }
 
-// The gradients of one batch entry's vectors from the partial sums; where shared gains have several
-// batch entries to add, the entry's P and Q replace its first slot for the next kernel.
+// The gradients of one batch entry's vectors from the partial sums, blockIdx.z of P, S and Q; where shared
+// gains have several batch entries to add, the entry's P and Q replace its first slot for the next kernel.
+// Latency is what counts, so the three sums and the slots go to as many threads as there are.
 __global__ void __launch_bounds__(kSumCols* kSumRows) sol_residual_norm_sum_kernel(const __grid_constant__ NormBwdArgs p,
                                                                                   int slots) {
-  const int b = blockIdx.y, cc = blockIdx.x * kSumCols + threadIdx.x;
+  const int b = blockIdx.y, which = blockIdx.z, cc = blockIdx.x * kSumCols + threadIdx.x;
   const bool on = cc < p.C;
   const int c = on ? cc : 0;
   const NormArgs& f = p.fwd;
-  float* part = p.part + static_cast<size_t>(b) * slots * 3 * p.C;
-  const size_t step = 3 * static_cast<size_t>(p.C);
+  float* part = p.part + static_cast<size_t>(b) * slots * 3 * p.C + static_cast<size_t>(which) * p.C;
+  const size_t step = 3 * static_cast<size_t>(p.C), at = static_cast<size_t>(b) * p.C + c;
   const bool first = threadIdx.y == 0 && on;
-  if (p.dscale != nullptr || p.dgain != nullptr) {
-    const float P = column_sum([&](int i) { return part[i * step + c]; }, slots);
-    if (first) {
-      if (p.dscale != nullptr) p.dscale[static_cast<size_t>(b) * p.C + c] = f.gain != nullptr ? f.gain[c] * P : P;
-      if (p.dgain != nullptr) {
-        const float one = f.scale != nullptr ? P * (1.0f + f.scale[static_cast<size_t>(b) * f.scale_stride + c]) : P;
-        if (f.B == 1) p.dgain[c] = one;
-        else part[c] = one;
-      }
-    }
+  float* own = which == 0 ? p.dscale : which == 1 ? p.dshift : p.dgate;
+  float* shared = which == 0 ? p.dgain : which == 2 ? p.dpost_gain : nullptr;
+  if (own == nullptr && shared == nullptr) return;
+  const float v = column_sum([&](int i) { return part[i * step + c]; }, slots);
+  if (!first) return;
+  if (own != nullptr) {
+    const float* gain = which == 0 ? f.gain : which == 2 ? f.post_gain : nullptr;
+    own[at] = gain != nullptr ? gain[c] * v : v;
   }
-  if (p.dshift != nullptr) {
-    const float S = column_sum([&](int i) { return part[i * step + p.C + c]; }, slots);
-    if (first) p.dshift[static_cast<size_t>(b) * p.C + c] = S;
-  }
-  if (p.dgate != nullptr || p.dpost_gain != nullptr) {
-    const float Q = column_sum([&](int i) { return part[i * step + 2 * static_cast<size_t>(p.C) + c]; }, slots);
-    if (first) {
-      if (p.dgate != nullptr) p.dgate[static_cast<size_t>(b) * p.C + c] = f.post_gain != nullptr ? f.post_gain[c] * Q : Q;
-      if (p.dpost_gain != nullptr) {
-        const float one = f.gate != nullptr ? Q * f.gate[static_cast<size_t>(b) * f.gate_stride + c] : Q;
-        if (f.B == 1) p.dpost_gain[c] = one;
-        else part[2 * static_cast<size_t>(p.C) + c] = one;
-      }
-    }
+  if (shared != nullptr) {
+    float one = v;
+    if (which == 0 && f.scale != nullptr) one = v * (1.0f + f.scale[static_cast<size_t>(b) * f.scale_stride + c]);
+    if (which == 2 && f.gate != nullptr) one = v * f.gate[static_cast<size_t>(b) * f.gate_stride + c];
+    if (f.B == 1) shared[c] = one;
+    else part[c] = one;
   }
 }
 
@@ -681,8 +674,10 @@ cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t s
   const size_t products = static_cast<size_t>(s.tpr) * E * 12;
   s.rpb = MAXT / s.tpr;
   if (s.tpr > 32 && s.rpb > 15) s.rpb = 15;
-  if (row > 0 && s.rpb > static_cast<long long>((kSmemMax - 10240 - products) / row))
-    s.rpb = static_cast<int>((kSmemMax - 10240 - products) / row);
+  if constexpr (RING) {
+    const long long fit = static_cast<long long>((kSmemMax - 10240 - products) / row);
+    if (s.rpb > fit) s.rpb = static_cast<int>(fit);
+  }
   if (s.rpb > a.T) s.rpb = a.T;
   if (s.rpb > share) s.rpb = static_cast<int>(share);
   if (s.tpr < 32) s.rpb = (s.rpb * s.tpr + 31) / 32 * 32 / s.tpr;  // whole warps
@@ -782,7 +777,7 @@ cudaError_t launch_residual_norm_bwd(const NormBwdArgs& a, cudaStream_t stream) 
   const int slots = a.chunks;
   const dim3 block(kSumCols, kSumRows);
   const unsigned cols = (a.C + kSumCols - 1) / kSumCols;
-  sol_residual_norm_sum_kernel<<<dim3(cols, f.B), block, 0, stream>>>(a, slots);
+  sol_residual_norm_sum_kernel<<<dim3(cols, f.B, 3), block, 0, stream>>>(a, slots);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (f.B > 1 && (a.dgain != nullptr || a.dpost_gain != nullptr)) {
     sol_residual_norm_sum_b_kernel<<<cols, block, 0, stream>>>(a, slots);

@@ -26,37 +26,75 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Turn per position of a pair, modulo one, as a 64-bit fraction.
-__device__ __forceinline__ unsigned long long turn_fraction(double inv_freq) {
+// Turn per position of a pair, modulo one, as a 64-bit fraction: hi 2^32 + lo with a signed lo.
+struct Fraction {
+  int hi, lo;
+};
+__device__ __forceinline__ Fraction turn_fraction(double inv_freq) {
   const double f = inv_freq * 0.15915494309189533577;  // over 2 pi
-  return __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
+  const unsigned long long u = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
+  const int lo = static_cast<int>(static_cast<uint32_t>(u));
+  return {static_cast<int>(static_cast<uint32_t>(u >> 32) + (lo < 0 ? 1u : 0u)), lo};
 }
-// m cos, m sin at a position.
-__device__ __forceinline__ void turn(int pos, unsigned long long fraction, float m, float& c, float& s) {
-  const uint32_t lo = static_cast<uint32_t>(fraction), hi = static_cast<uint32_t>(fraction >> 32);
-  uint32_t a = static_cast<uint32_t>(pos) * hi + __umulhi(static_cast<uint32_t>(pos), lo);
-  if (pos < 0) a -= lo;  // the product of a negative position, as its low 32 bits are above 0
-  const uint32_t quarter = (a + 0x20000000u) >> 30;
-  const float x = static_cast<float>(static_cast<int>(a - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi 2^-32: |x| <= pi / 4
-  const float q = x * x;
+// The top 32 bits of a position's angle, in turns; wraps as turns do.
+__device__ __forceinline__ uint32_t angle_of(int pos, const Fraction& f) {
+  return static_cast<uint32_t>(pos) * static_cast<uint32_t>(f.hi) + static_cast<uint32_t>(__mulhi(pos, f.lo));
+}
+// m cos, m sin of two angles.
+__device__ __forceinline__ void turn2(uint32_t a0, uint32_t a1, float m, float (&c)[2], float (&s)[2]) {
+  const uint32_t a[2] = {a0, a1};
+  uint32_t quarter[2];
+  float r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    quarter[i] = a[i] + 0x20000000u;  // the nearest quarter turn, in its top two bits
+    r[i] = static_cast<float>(static_cast<int>(a[i] - (quarter[i] & 0xc0000000u)));
+  }
+  auto two = [](float v) { return pack2(v, v); };
+  const f2 x = mul2(pack2(r[0], r[1]), two(1.4629180792671596e-9f));  // 2 pi 2^-32: |x| <= pi / 4
+  const f2 q = mul2(x, x);
   // degrees 9 and 10: the next terms are below 2e-9 and 2e-10 of the first
-  float sn = fmaf(q, 2.7557319e-6f, -1.9841270e-4f);
-  sn = fmaf(sn, q, 8.3333333e-3f);
-  sn = fmaf(sn, q, -1.6666667e-1f);
-  sn = fmaf(sn * q, x, x);
-  float cs = fmaf(q, -2.7557319e-7f, 2.4801587e-5f);
-  cs = fmaf(cs, q, -1.3888889e-3f);
-  cs = fmaf(cs, q, 4.1666667e-2f);
-  cs = fmaf(cs, q, -0.5f);
-  cs = fmaf(cs, q, 1.0f);
-  const float cc = (quarter & 1u) ? sn : cs, ss = (quarter & 1u) ? cs : sn;  // cos(x + pi/2) = -sin x, ..
-  c = ((quarter + 1u) & 2u) ? -m * cc : m * cc;
-  s = (quarter & 2u) ? -m * ss : m * ss;
+  f2 sn = fma2(q, two(2.7557319e-6f), two(-1.9841270e-4f));
+  sn = fma2(sn, q, two(8.3333333e-3f));
+  sn = fma2(sn, q, two(-1.6666667e-1f));
+  sn = fma2(mul2(sn, q), x, x);
+  f2 cs = fma2(q, two(-2.7557319e-7f), two(2.4801587e-5f));
+  cs = fma2(cs, q, two(-1.3888889e-3f));
+  cs = fma2(cs, q, two(4.1666667e-2f));
+  cs = fma2(cs, q, two(-0.5f));
+  cs = fma2(cs, q, two(1.0f));
+  const float2 sv = unpack2(mul2(sn, two(m))), cv = unpack2(mul2(cs, two(m)));
+  const float ss[2] = {sv.x, sv.y}, cc[2] = {cv.x, cv.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // cos(x + pi / 2) = -sin x, sin(x + pi / 2) = cos x, and their negatives
+    const bool odd = (quarter[i] & 0x40000000u) != 0;
+    const uint32_t neg_s = quarter[i] & 0x80000000u, neg_c = (quarter[i] + 0x40000000u) & 0x80000000u;
+    c[i] = __uint_as_float(__float_as_uint(odd ? ss[i] : cc[i]) ^ neg_c);
+    s[i] = __uint_as_float(__float_as_uint(odd ? cc[i] : ss[i]) ^ neg_s);
+  }
 }
 __device__ __forceinline__ int axis_of(const int (&end)[4], int i) { return (i >= end[0]) + (i >= end[1]) + (i >= end[2]); }
-__device__ __forceinline__ void turn_of(const RopeArgs& p, int b, int t, int i, float& c, float& s) {
-  turn(__ldg(p.pos + b * p.pos_b + static_cast<size_t>(axis_of(p.end, i)) * p.L + t), turn_fraction(__ldg(p.inv_freq + i)),
-       p.factor, c, s);
+// m cos, m sin of the pairs i .. i + N - 1 of a token, those past the last with cosine m and sine 0.
+template <int N>
+__device__ __forceinline__ void turns_of(const RopeArgs& p, int b, int t, int i, int last, float (&c)[N], float (&s)[N]) {
+  uint32_t a[N + 1];
+  a[N] = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    a[k] = i + k < last ? angle_of(__ldg(p.pos + b * p.pos_b + static_cast<size_t>(axis_of(p.end, i + k)) * p.L + t),
+                                   turn_fraction(__ldg(p.inv_freq + i + k)))
+                        : 0u;
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float cc[2], ss[2];
+    turn2(a[k], a[k + 1], p.factor, cc, ss);
+    c[k] = cc[0];
+    s[k] = p.inverse ? -ss[0] : ss[0];
+    if (k + 1 < N) {
+      c[k + 1] = cc[1];
+      s[k + 1] = p.inverse ? -ss[1] : ss[1];
+    }
+  }
 }
 
 template <typename T, int V>
@@ -140,13 +178,7 @@ __global__ void __launch_bounds__(kThreads) sol_rope_interleaved_kernel(const __
   }
   const int turned = min(V, p.rot - col);  // a vector across the border: its first values turn
   float c[V / 2], s[V / 2];
-#pragma unroll
-  for (int k = 0; k < V / 2; ++k) {
-    c[k] = 1.f;
-    s[k] = 0.f;
-    if (2 * k < turned) turn_of(p, b, t, col / 2 + k, c[k], s[k]);
-    if (p.inverse) s[k] = -s[k];
-  }
+  turns_of<V / 2>(p, b, t, col / 2, p.rot / 2, c, s);
   for_heads<T>(p, b, t, h0, h1, [&](const T* in, T* out, long long ih, long long oh, int lo, int hi) {
 #pragma unroll 4
     for (int h = lo; h < hi; ++h) {
@@ -174,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) sol_rope_interleaved_kernel(const __
 
 // Half layout: V pairs per thread, (i, i + rot / 2); groups past those copy V channels of the rest.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) sol_rope_half_kernel(const __grid_constant__ RopeArgs p, int groups,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 5 : 4) sol_rope_half_kernel(const __grid_constant__ RopeArgs p, int groups,
                                                                   int heads_per_block) {
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int t = static_cast<int>(i / groups), g = static_cast<int>(i - static_cast<long long>(t) * groups);
@@ -192,11 +224,7 @@ __global__ void __launch_bounds__(kThreads) sol_rope_half_kernel(const __grid_co
   }
   const int col = g * V;
   float c[V], s[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    turn_of(p, b, t, col + k, c[k], s[k]);
-    if (p.inverse) s[k] = -s[k];
-  }
+  turns_of<V>(p, b, t, col, half, c, s);
   for_heads<T>(p, b, t, h0, h1, [&](const T* in, T* out, long long ih, long long oh, int lo, int hi) {
 #pragma unroll 4
     for (int h = lo; h < hi; ++h) {
@@ -238,26 +266,52 @@ cudaError_t launch_t(const RopeArgs& a, int num_sms, cudaStream_t stream) {
 // Tables: V pairs of one token per thread and turn of the loop, the same pairs every time, so that
 // their fractions stay in registers. Bound by the stores.
 template <int V>
-__global__ void __launch_bounds__(kThreads) sol_rope_tables_kernel(const __grid_constant__ RopeTableArgs p, int groups, int tokens) {
+__global__ void __launch_bounds__(kThreads) sol_rope_tables_kernel(const __grid_constant__ RopeTableArgs p, int groups, int tokens,
+                                                                    int share) {
   const int half = p.rot / 2, g = threadIdx.x % groups;
   if (threadIdx.x >= groups * tokens) return;
+  // a block's tokens lie together: their positions share cache lines
+  const long long from = static_cast<long long>(blockIdx.x) * share;
+  const int t_end = static_cast<int>(from + share < p.L ? from + share : p.L);
+  if (from + threadIdx.x / groups >= t_end) return;
+  const int t_first = static_cast<int>(from) + threadIdx.x / groups;
   for (int j = g * V; j < half; j += groups * V) {
-    unsigned long long f[V];
+    Fraction f[V];
     const int* pos[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       f[k] = turn_fraction(__ldg(p.inv_freq + j + k));
       pos[k] = p.pos + static_cast<size_t>(axis_of(p.end, j + k)) * p.L;
     }
-    const long long step = static_cast<long long>(gridDim.x) * tokens;
-    for (long long t = static_cast<long long>(blockIdx.x) * tokens + threadIdx.x / groups; t < p.L; t += step) {
-      float c[V], s[V];
+    const bool one_axis = pos[0] == pos[V - 1];
+    int next[V];
+    auto read = [&](int t) {
+      if (t >= t_end) return;
+      next[0] = __ldg(pos[0] + t);
 #pragma unroll
-      for (int k = 0; k < V; ++k) turn(__ldg(pos[k] + t), f[k], p.factor, c[k], s[k]);
+      for (int k = 1; k < V; ++k) next[k] = one_axis ? next[0] : __ldg(pos[k] + t);
+    };
+    read(t_first);
+    for (int t = t_first; t < t_end; t += tokens) {
+      uint32_t a[V + 1];
+      a[V] = 0;
+#pragma unroll
+      for (int k = 0; k < V; ++k) a[k] = angle_of(next[k], f[k]);
+      read(t + tokens);
+      float c[V + 1], s[V + 1];
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        float cc[2], ss[2];
+        turn2(a[k], a[k + 1], p.factor, cc, ss);
+        c[k] = cc[0];
+        s[k] = ss[0];
+        c[k + 1] = cc[1];
+        s[k + 1] = ss[1];
+      }
       const size_t o = static_cast<size_t>(t) * half + j;
       if constexpr (V == 4) {
-        *reinterpret_cast<float4*>(p.cos + o) = make_float4(c[0], c[1], c[2], c[3]);
-        *reinterpret_cast<float4*>(p.sin + o) = make_float4(s[0], s[1], s[2], s[3]);
+        __stcs(reinterpret_cast<float4*>(p.cos + o), make_float4(c[0], c[1], c[2], c[3]));
+        __stcs(reinterpret_cast<float4*>(p.sin + o), make_float4(s[0], s[1], s[2], s[3]));
       } else {
         p.cos[o] = c[0];
         p.sin[o] = s[0];
@@ -277,10 +331,12 @@ cudaError_t launch_rope_tables(const RopeTableArgs& a, int num_sms, cudaStream_t
   const int half = a.rot / 2;
   const bool vec = half % 4 == 0 && (reinterpret_cast<uintptr_t>(a.cos) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.sin) & 15u) == 0;
   const int per_token = vec ? half / 4 : half, groups = per_token < kThreads ? per_token : kThreads, tokens = kThreads / groups;
-  const long long blocks = (static_cast<long long>(a.L) + tokens - 1) / tokens, most = 8ll * num_sms;
-  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  if (vec) sol_rope_tables_kernel<4><<<grid, kThreads, 0, stream>>>(a, groups, tokens);
-  else sol_rope_tables_kernel<1><<<grid, kThreads, 0, stream>>>(a, groups, tokens);
+  // four blocks per SM, each with an equal run of whole turns
+  const long long turns = (static_cast<long long>(a.L) + tokens - 1) / tokens, per = (turns + 4ll * num_sms - 1) / (4ll * num_sms);
+  const unsigned grid = static_cast<unsigned>((turns + per - 1) / per);
+  const int share = static_cast<int>(per * tokens);
+  if (vec) sol_rope_tables_kernel<4><<<grid, kThreads, 0, stream>>>(a, groups, tokens, share);
+  else sol_rope_tables_kernel<1><<<grid, kThreads, 0, stream>>>(a, groups, tokens, share);
   return cudaGetLastError();
 }
 
