@@ -563,9 +563,25 @@ def tau_list(values) -> list:
 # ---- dense operators around the attention ----------------------------------------------------------
 
 # These calls can be as short as a few microseconds on the device, so what the host does per call counts:
-# addresses go to ctypes as plain integers, the stream comes as its raw handle, and outputs are made
-# by an input's new_empty or empty_like. Together they took a call on one token from 22 to 16 us.
+# addresses go to ctypes as plain integers, the stream comes as its raw handle, outputs are made by an
+# input's new_empty or empty_like, and each tensor is asked one whole question (_fits) before the checks
+# that find out what is wrong with it. Together they took a call on four tokens from 22 to 15 us.
 _I64x3 = ctypes.c_int64 * 3
+_F32, _BF16 = torch.float32, torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _fits(t, index: int, dtype, shape) -> bool:
+    """A contiguous tensor on CUDA device `index` of the given dtype and shape?"""
+    try:
+        return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    except (AttributeError, RuntimeError):
+        return False
+
+
+def _elsewhere(x, stream) -> bool:
+    """Does a call on x have to change the current device or stream first?"""
+    return stream is not None or torch.cuda.current_device() != x.get_device()
 
 
 def _addr(t):
@@ -594,7 +610,6 @@ class _On:
             self._contexts = (torch.cuda.device(self.device),)
         for c in self._contexts:
             c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(index)
 
     def __exit__(self, *exc):
         for c in self._contexts:
@@ -614,6 +629,8 @@ def _need_cuda_on(name: str, t, device, dtype=None) -> None:
 
 def _need_like(name: str, t, ref) -> None:
     """A contiguous CUDA tensor of ref's device, dtype and shape."""
+    if _fits(t, ref.get_device(), ref.dtype, ref.shape):
+        return
     _need_cuda_on(name, t, ref.device, ref.dtype)
     if t.shape != ref.shape:
         raise ValueError(f"{name} must have shape {tuple(ref.shape)}, got {tuple(t.shape)}")
@@ -622,7 +639,7 @@ def _need_like(name: str, t, ref) -> None:
 
 
 def _need_vector(name: str, t, device, C: int) -> None:
-    if t is None:
+    if t is None or _fits(t, device.index, _F32, (C,)):
         return
     _need_cuda_on(name, t, device, torch.float32)
     if t.shape != (C,) or not t.is_contiguous():
@@ -633,7 +650,8 @@ def _need_rows(name: str, t, device, B: int, C: int) -> int:
     """Checks [B, C] fp32 rows (channels contiguous) and returns their stride."""
     if t is None:
         return 0
-    _need_cuda_on(name, t, device, torch.float32)
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index or t.dtype is not _F32:
+        _need_cuda_on(name, t, device, _F32)
     if t.shape != (B, C):
         raise ValueError(f"{name} must be [B, C] = [{B}, {C}], got {tuple(t.shape)}")
     row, channel = t.stride()
@@ -645,7 +663,7 @@ def _need_rows(name: str, t, device, B: int, C: int) -> int:
 def _choice(name: str, value, names: dict) -> int:
     try:
         return names[value]
-    except (KeyError, TypeError):
+    except (KeyError, TypeError):  # TypeError: not hashable
         raise ValueError(f"{name} must be one of {sorted(names)}, got {value!r}") from None
 
 
@@ -675,15 +693,20 @@ def sol_attn_residual_norm(x, y=None, gate=None, gain=None, scale=None, shift=No
         _need_like("x_out", x_out, x)
     if h is not None:
         _need_like("h", h, x)
-    with _On(x.device, stream) as s:
-        if y is not None and x_out is None:
-            x_out = torch.empty_like(x)
-        if h is None:
-            h = torch.empty_like(x)
-        st = load_library().sol_attn_residual_norm(
-            _addr(x), _addr(y), _addr(gate), gs, _addr(gain), _addr(scale), ss, _addr(shift), hs, _addr(post_gain), dt, n, pn,
-            res_scale, eps, B, T, C, _addr(x_out), _addr(h), s)
-    _check(st, "sol_attn_residual_norm")
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return sol_attn_residual_norm(x, y, gate, gain, scale, shift, post_gain, norm, post_norm, res_scale, eps, x_out, h)
+    if y is not None and x_out is None:
+        x_out = torch.empty_like(x)
+    if h is None:
+        h = torch.empty_like(x)
+    st = load_library().sol_attn_residual_norm(
+        x.data_ptr(), None if y is None else y.data_ptr(), None if gate is None else gate.data_ptr(), gs,
+        None if gain is None else gain.data_ptr(), None if scale is None else scale.data_ptr(), ss,
+        None if shift is None else shift.data_ptr(), hs, None if post_gain is None else post_gain.data_ptr(), dt, n, pn,
+        res_scale, eps, B, T, C, None if x_out is None else x_out.data_ptr(), h.data_ptr(), _raw_stream(x.get_device()))
+    if st != SOL_OK:
+        _check(st, "sol_attn_residual_norm")
     return (x if y is None else x_out), h
 
 
@@ -699,27 +722,27 @@ def sol_attn_residual_norm_bwd(dh, x, y=None, gate=None, gain=None, scale=None, 
     _need_like("dh", dh, x)
     if dx_out is not None:
         _need_like("dx_out", dx_out, x)
-    if workspace is not None:
-        _need_cuda_on("workspace", workspace, x.device, torch.uint8)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+    _error_words(workspace, x.device)
     want_dshift = scale is not None if want_dshift is None else want_dshift
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return sol_attn_residual_norm_bwd(dh, x, y, gate, gain, scale, post_gain, dx_out, norm, post_norm, res_scale, eps,
+                                              want_dshift, workspace)
     lib = load_library()
-    with _On(x.device, stream) as s:
-        def new(want, *shape):
-            return x.new_empty(shape, dtype=torch.float32) if want else None
-        g = {"dx": torch.empty_like(x), "dy": None if y is None else torch.empty_like(x),
-             "dgate": new(gate is not None, B, C), "dgain": new(gain is not None, C),
-             "dscale": new(scale is not None, B, C), "dshift": new(want_dshift, B, C),
-             "dpost_gain": new(post_gain is not None, C)}
-        if workspace is None and any(g[k] is not None for k in ("dgate", "dgain", "dscale", "dshift", "dpost_gain")):
-            workspace = x.new_empty(lib.sol_attn_residual_norm_bwd_workspace_bytes(B, T, C), dtype=torch.uint8)
-        st = lib.sol_attn_residual_norm_bwd(
-            _addr(dh), _addr(dx_out), _addr(x), _addr(y), _addr(gate), gs, _addr(gain), _addr(scale), ss, _addr(post_gain), dt, n,
-            pn, res_scale, eps, B, T, C, _addr(g["dx"]), _addr(g["dy"]), _addr(g["dgate"]), _addr(g["dgain"]),
-            _addr(g["dscale"]), _addr(g["dshift"]), _addr(g["dpost_gain"]), _addr(workspace),
-            0 if workspace is None else workspace.numel(), s)
-    _check(st, "sol_attn_residual_norm_bwd")
+
+    def new(want, *shape):
+        return x.new_empty(shape, dtype=_F32) if want else None
+    g = {"dx": torch.empty_like(x), "dy": None if y is None else torch.empty_like(x),
+         "dgate": new(gate is not None, B, C), "dgain": new(gain is not None, C),
+         "dscale": new(scale is not None, B, C), "dshift": new(want_dshift, B, C),
+         "dpost_gain": new(post_gain is not None, C)}
+    if workspace is None and (gate is not None or gain is not None or scale is not None or want_dshift or post_gain is not None):
+        workspace = x.new_empty(lib.sol_attn_residual_norm_bwd_workspace_bytes(B, T, C), dtype=torch.uint8)
+    a = [None if t is None else t.data_ptr() for t in (dh, dx_out, x, y, gate, gain, scale, post_gain, *g.values(), workspace)]
+    st = lib.sol_attn_residual_norm_bwd(*a[:5], gs, *a[5:7], ss, a[7], dt, n, pn, res_scale, eps, B, T, C, *a[8:],
+                                        0 if workspace is None else workspace.numel(), _raw_stream(x.get_device()))
+    if st != SOL_OK:
+        _check(st, "sol_attn_residual_norm_bwd")
     return g
 
 
@@ -745,14 +768,16 @@ def sol_attn_rope_inv_freq(rot: int, base: float = 10000.0, sections=None, scali
 
 def _check_positions(pos, inv_freq, sections, device, L: int, B: Optional[int]):
     """(axes, sections array, stride of a batch entry's positions)."""
-    _need_cuda_on("pos", pos, device, torch.int32)
-    _need_cuda_on("inv_freq", inv_freq, device, torch.float64)
-    if not pos.is_contiguous() or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
-        raise ValueError("pos and inv_freq must be contiguous, inv_freq a vector")
     axes = len(sections) if sections is not None else 1
-    shapes = [(axes, L)] + ([(L,)] if axes == 1 else []) + ([(B, axes, L)] if B is not None else [])
-    if tuple(pos.shape) not in shapes:
-        raise ValueError(f"pos must have one of the shapes {shapes}, got {tuple(pos.shape)}")
+    if not (_fits(pos, device.index, torch.int32, (axes, L)) and inv_freq.get_device() == device.index and
+            inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+        _need_cuda_on("pos", pos, device, torch.int32)
+        _need_cuda_on("inv_freq", inv_freq, device, torch.float64)
+        if not pos.is_contiguous() or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+            raise ValueError("pos and inv_freq must be contiguous, inv_freq a vector")
+        shapes = [(axes, L)] + ([(L,)] if axes == 1 else []) + ([(B, axes, L)] if B is not None else [])
+        if tuple(pos.shape) not in shapes:
+            raise ValueError(f"pos must have one of the shapes {shapes}, got {tuple(pos.shape)}")
     return axes, _int_array(sections), (axes * L if pos.dim() == 3 else 0)
 
 
@@ -770,12 +795,15 @@ def sol_attn_rope_tables(pos, inv_freq, sections=None, attn_factor: float = 1.0,
             _need_cuda_on(n, t, dev, torch.float32)
             if tuple(t.shape) != (L, half) or not t.is_contiguous():
                 raise ValueError(f"{n} must be a contiguous [{L}, {half}] tensor")
-    with _On(dev, stream) as s:
-        rope_cos = pos.new_empty((L, half), dtype=torch.float32) if rope_cos is None else rope_cos
-        rope_sin = pos.new_empty((L, half), dtype=torch.float32) if rope_sin is None else rope_sin
-        st = load_library().sol_attn_rope_tables(_addr(pos), axes, sec, _addr(inv_freq), attn_factor, L, 2 * half,
-                                                 _addr(rope_cos), _addr(rope_sin), s)
-    _check(st, "sol_attn_rope_tables")
+    if _elsewhere(pos, stream):
+        with _On(dev, stream):
+            return sol_attn_rope_tables(pos, inv_freq, sections, attn_factor, rope_cos, rope_sin)
+    rope_cos = pos.new_empty((L, half), dtype=_F32) if rope_cos is None else rope_cos
+    rope_sin = pos.new_empty((L, half), dtype=_F32) if rope_sin is None else rope_sin
+    st = load_library().sol_attn_rope_tables(pos.data_ptr(), axes, sec, inv_freq.data_ptr(), attn_factor, L, 2 * half,
+                                             rope_cos.data_ptr(), rope_sin.data_ptr(), _raw_stream(pos.get_device()))
+    if st != SOL_OK:
+        _check(st, "sol_attn_rope_tables")
     return rope_cos, rope_sin
 
 
@@ -791,35 +819,42 @@ def sol_attn_rope(Q, K, pos, inv_freq, layout: str = "interleaved", sections=Non
         raise ValueError("Q must be [B, Hq, L, d]")
     B, Hq, L, d = Q.shape
     dt, lay = _dtype_code(Q), _choice("layout", layout, ROPE_LAYOUTS)
+    index, dtype = Q.get_device(), Q.dtype
     if K is None:
         if K_out is not None:
             raise ValueError("K_out needs K")
     else:
-        _need_cuda_on("K", K, Q.device, Q.dtype)
-        if K.dim() != 4 or K.shape[0] != B or tuple(K.shape[2:]) != (L, d):
+        if not isinstance(K, torch.Tensor) or K.get_device() != index or K.dtype is not dtype:
+            _need_cuda_on("K", K, Q.device, dtype)
+        if K.dim() != 4 or K.shape[0] != B or K.shape[2] != L or K.shape[3] != d:
             raise ValueError("K must be [B, Hk, L, d] with the B, L and d of Q")
     for n, t, ref in (("Q_out", Q_out, Q), ("K_out", K_out, K)):
         if t is not None:
-            _need_cuda_on(n, t, Q.device, Q.dtype)
+            _need_cuda_on(n, t, Q.device, dtype)
             if t.shape != ref.shape:
                 raise ValueError(f"{n} must have shape {tuple(ref.shape)}")
-    for n, t in (("Q", Q), ("K", K), ("Q_out", Q_out), ("K_out", K_out)):
-        if t is not None and d > 1 and t.stride(3) != 1:
-            raise ValueError(f"{n}'s channels must be contiguous")
     axes, sec, pos_b = _check_positions(pos, inv_freq, sections, Q.device, L, B)
+    if _elsewhere(Q, stream):
+        with _On(Q.device, stream):
+            return sol_attn_rope(Q, K, pos, inv_freq, layout, sections, attn_factor, inverse, Q_out, K_out)
+    if Q_out is None:
+        Q_out = torch.empty_like(Q, memory_format=torch.contiguous_format)
+    if K is not None and K_out is None:
+        K_out = torch.empty_like(K, memory_format=torch.contiguous_format)
 
-    def strides(t):
-        return None if t is None else _I64x3(*t.stride()[:3])
-    with _On(Q.device, stream) as s:
-        if Q_out is None:
-            Q_out = torch.empty_like(Q, memory_format=torch.contiguous_format)
-        if K is not None and K_out is None:
-            K_out = torch.empty_like(K, memory_format=torch.contiguous_format)
-        st = load_library().sol_attn_rope(
-            _addr(Q), strides(Q), _addr(K), strides(K), dt, _addr(pos), pos_b, axes, sec, _addr(inv_freq), attn_factor, lay,
-            int(bool(inverse)), B, Hq, 0 if K is None else K.shape[1], L, d, 2 * inv_freq.numel(), _addr(Q_out),
-            strides(Q_out), _addr(K_out), strides(K_out), s)
-    _check(st, "sol_attn_rope")
+    def rows(name, t):
+        if t is None:
+            return None, None
+        b, h, l, c = t.stride()
+        if d > 1 and c != 1:
+            raise ValueError(f"{name}'s channels must be contiguous")
+        return t.data_ptr(), _I64x3(b, h, l)
+    st = load_library().sol_attn_rope(
+        *rows("Q", Q), *rows("K", K), dt, pos.data_ptr(), pos_b, axes, sec, inv_freq.data_ptr(), attn_factor, lay,
+        1 if inverse else 0, B, Hq, 0 if K is None else K.shape[1], L, d, 2 * inv_freq.numel(), *rows("Q_out", Q_out),
+        *rows("K_out", K_out), _raw_stream(index))
+    if st != SOL_OK:
+        _check(st, "sol_attn_rope")
     return Q_out, K_out
 
 
@@ -827,11 +862,13 @@ def _check_linear(first: str, a, w, x=None):
     """Shapes of a product's bf16 operands: leading shape, M, N, K. `a` is x or, with x given apart, dy."""
     if not isinstance(a, torch.Tensor) or not a.is_cuda:
         raise TypeError(f"{first} must be a CUDA tensor")
+    index = a.get_device()
     for n, t in ((first, a), ("w", w), ("x", x)):
         if t is None:
             continue
-        _need_cuda_on(n, t, a.device, torch.bfloat16)
-        if t.dim() < 1 or not t.is_contiguous():
+        if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype is not _BF16:
+            _need_cuda_on(n, t, a.device, _BF16)
+        if not t.is_contiguous() or t.dim() < 1:
             raise ValueError(f"{n} must be contiguous")
     if w is not None and w.dim() != 2:
         raise ValueError("w must be [N, K]")
@@ -860,20 +897,25 @@ def sol_attn_linear(x, w, bias=None, act: str = "none", residual=None, out=None,
     for n in x.shape[:-1]:
         M *= n
     _need_vector("bias", bias, x.device, N)
+    index = x.get_device()
     for n, t in (("residual", residual), ("out", out), ("z", z)):
-        if t is not None:
-            _need_cuda_on(n, t, x.device, torch.bfloat16)
-            if t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"{n} must be contiguous with shape {tuple(shape)}")
+        if t is not None and not _fits(t, index, _BF16, shape):
+            _need_cuda_on(n, t, x.device, _BF16)
+            raise ValueError(f"{n} must be contiguous with shape {tuple(shape)}")
     _error_words(workspace, x.device)
-    with _On(x.device, stream) as s:
-        if out is None:
-            out = x.new_empty(shape)
-        if z is None and want_z:
-            z = x.new_empty(shape)
-        st = load_library().sol_attn_linear(_addr(x), _addr(w), _addr(bias), _addr(residual), code, M, N, K, _addr(out), _addr(z),
-                                            _addr(workspace), 0 if workspace is None else workspace.numel(), s)
-    _check(st, "sol_attn_linear")
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return sol_attn_linear(x, w, bias, act, residual, out, z, want_z, workspace)
+    if out is None:
+        out = x.new_empty(shape)
+    if z is None and want_z:
+        z = x.new_empty(shape)
+    st = load_library().sol_attn_linear(
+        x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+        None if residual is None else residual.data_ptr(), code, M, N, K, out.data_ptr(), None if z is None else z.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), _raw_stream(index))
+    if st != SOL_OK:
+        _check(st, "sol_attn_linear")
     return out if z is None else (out, z)
 
 
@@ -892,14 +934,17 @@ def sol_attn_linear_bwd(dy, x, w, z=None, act: str = "none", want_dx: bool = Tru
     if z is not None:
         _need_like("z", z, dy)
     _error_words(workspace, dy.device)
+    if _elsewhere(dy, stream):
+        with _On(dy.device, stream):
+            return sol_attn_linear_bwd(dy, x, w, z, act, want_dx, want_dw, want_db, workspace)
     lib = load_library()
-    with _On(dy.device, stream) as s:
-        dx = torch.empty_like(x) if want_dx else None
-        dw = torch.empty_like(w) if want_dw else None
-        db = dy.new_empty(N, dtype=torch.float32) if want_db else None
-        if workspace is None:
-            workspace = dy.new_empty(lib.sol_attn_linear_bwd_workspace_bytes(M, N, code), dtype=torch.uint8)
-        st = lib.sol_attn_linear_bwd(_addr(dy), _addr(x), _addr(w), _addr(z), code, M, N, K, _addr(dx), _addr(dw), _addr(db),
-                                     _addr(workspace), workspace.numel(), s)
-    _check(st, "sol_attn_linear_bwd")
+    dx = torch.empty_like(x) if want_dx else None
+    dw = torch.empty_like(w) if want_dw else None
+    db = dy.new_empty(N, dtype=_F32) if want_db else None
+    if workspace is None:
+        workspace = dy.new_empty(lib.sol_attn_linear_bwd_workspace_bytes(M, N, code), dtype=torch.uint8)
+    st = lib.sol_attn_linear_bwd(_addr(dy), _addr(x), _addr(w), _addr(z), code, M, N, K, _addr(dx), _addr(dw), _addr(db),
+                                 _addr(workspace), workspace.numel(), _raw_stream(dy.get_device()))
+    if st != SOL_OK:
+        _check(st, "sol_attn_linear_bwd")
     return dx, dw, db
