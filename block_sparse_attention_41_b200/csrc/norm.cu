@@ -25,6 +25,7 @@ namespace sol {
 namespace {
 
 constexpr int kMaxWarps = 16;  // of a row
+constexpr int kSlot = 512;     // 16 bytes of each of a warp's threads
 constexpr int kMaxRows = 16;   // of several warps in a block: 15 named barriers
 constexpr int kSmemMax = 227 * 1024;  // per block
 
@@ -79,24 +80,28 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
 }
 
 // The E channels of a row that a thread owns, E / V vectors of V consecutive ones (V = 8 or 4: 16
-// bytes; V = 1: single values), and its part of shared memory: 16-byte slots, one per thread side by
-// side. FULL: every vector lies within the row, and a row has whole warps. Rows are addressed by the byte offset of the thread's
-// first channel, which the loops carry along: forming it anew costs more than the arithmetic.
+// bytes; V = 1: single values), and its part of shared memory: 16-byte slots, a warp's side by side.
+// A warp's channels lie together, so that a thread's vectors and slots are at fixed distances: rows
+// are addressed by the byte offset of the thread's first channel, which the loops carry along, and
+// everything else is an immediate (address arithmetic was a third of the instructions before).
+// FULL: every vector lies within the row, and a row has whole warps.
 template <typename T, int V, int E, bool FULL>
 struct Lane {
   static constexpr int NV = E / V, P = E / 2;
   static constexpr bool kFull = FULL;
-  int tpr, t, C;
-  uint32_t smem, step;
+  int first, side, C;  // first channel; threads side by side (32, or a shorter row's)
+  uint32_t smem;
 
-  __device__ __forceinline__ int chan(int j) const { return (j * tpr + t) * V; }
+  __device__ __forceinline__ Lane(int tpr, int t, int C, uint32_t smem)
+      : first(t / 32 * 32 * E + t % 32 * V), side(tpr < 32 ? tpr : 32), C(C), smem(smem) {}
+  __device__ __forceinline__ int chan(int j) const { return first + j * (FULL ? 32 : side) * V; }
   __device__ __forceinline__ bool on(int j) const { return FULL || chan(j) < C; }
-  __device__ __forceinline__ uint32_t slot(int i) const { return smem + static_cast<uint32_t>(i) * step; }
+  __device__ __forceinline__ uint32_t slot(int i) const { return smem + static_cast<uint32_t>(i) * kSlot; }
   __device__ __forceinline__ const T* at(const void* base, size_t o, int j) const {
-    return reinterpret_cast<const T*>(static_cast<const char*>(base) + o + j * tpr * V * static_cast<int>(sizeof(T)));
+    return reinterpret_cast<const T*>(static_cast<const char*>(base) + o + j * (FULL ? 32 : side) * V * static_cast<int>(sizeof(T)));
   }
   __device__ __forceinline__ T* at(void* base, size_t o, int j) const {
-    return reinterpret_cast<T*>(static_cast<char*>(base) + o + j * tpr * V * static_cast<int>(sizeof(T)));
+    return reinterpret_cast<T*>(static_cast<char*>(base) + o + j * (FULL ? 32 : side) * V * static_cast<int>(sizeof(T)));
   }
 
   // a row from global memory
@@ -135,14 +140,14 @@ struct Lane {
     if constexpr (V > 1) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (on(j)) cp_async16(to + j * step, at(base, o, j));
+        if (on(j)) cp_async16(to + j * kSlot, at(base, o, j));
     }
   }
   __device__ __forceinline__ void take(uint32_t from, f2 (&x)[P]) const {
     if constexpr (V > 1) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (on(j)) widen<V>(lds128(from + j * step), &x[j * V / 2]);
+        if (on(j)) widen<V>(lds128(from + j * kSlot), &x[j * V / 2]);
     }
   }
   // an fp32 vector (16-byte aligned where V > 1); channels past C and an absent vector read as `absent`
@@ -294,22 +299,24 @@ __device__ __forceinline__ void normalise_back(const L& l, RowGroup& g, f2 (&w)[
 // ---- forward ---------------------------------------------------------------------------------------
 // A block's groups of tpr threads take rows of one batch entry, so they share the vectors' products in
 // shared memory: A = gate post_gain, S = gain (1 + scale), H = shift. (In registers they left room
-// for half as many threads and spilled: 874 us at 75600 x 5120 bf16; read per row from L1, 793 us.)
+// for half as many threads and spilled: 874 us at 75600 x 5120 bf16; read per row from L1, 793 us; this
+// form 479 us, 6.5 TB/s.)
 // RING: the next row is on its way while one is reduced; else direct loads.
 template <typename T, int V, int E, bool RING, bool FULL, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid_constant__ NormArgs p, int tpr, int chunks) {
   using L = Lane<T, V, E, FULL>;
   constexpr int kParam = E / 4;  // slots of a product
-  extern __shared__ uint4 s_mem[];  // products [3][kParam][tpr], ring [R][tensors][NV][threads]
+  extern __shared__ uint4 s_mem[];  // per warp of a row products [3][kParam], per warp of the block ring [2][2][NV], in slots
   __shared__ float s_buf[kMaxRows * 4 * kMaxWarps];
   RowGroup g = row_group(s_buf, tpr);
   const int rpb = blockDim.x / tpr, t = threadIdx.x - g.sub * tpr;
-  const uint32_t ring = smem_u32(s_mem) + 3 * kParam * tpr * 16 + threadIdx.x * 16;
-  const L l{tpr, t, p.C, ring, blockDim.x * 16u};
+  const uint32_t prod = smem_u32(s_mem) + (t / 32 * 3 * kParam * kSlot + t % 32 * 16);
+  const uint32_t ring = smem_u32(s_mem) + ((tpr + 31) / 32 * 3 * kParam + threadIdx.x / 32 * 4 * L::NV) * kSlot + threadIdx.x % 32 * 16;
+  const L l(tpr, t, p.C, ring);
   const int b = blockIdx.x / chunks, chunk = blockIdx.x - b * chunks;
   const float inv_c = 1.0f / static_cast<float>(p.C);
   const bool has_y = p.y != nullptr;
-  const uint32_t slot_bytes = (has_y ? 2 : 1) * L::NV * l.step;
+  constexpr uint32_t slot_bytes = 2 * L::NV * kSlot;
   const int stride = chunks * rpb;  // a block's last rows may be past the end
   const size_t step = static_cast<size_t>(stride) * p.C * sizeof(T);
   int row = chunk * rpb + g.sub;
@@ -317,17 +324,16 @@ __global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid
   auto fetch = [&](int r, size_t from, uint32_t to) {
     if (r < p.T) {
       l.fetch(p.x, from, to);
-      if (has_y) l.fetch(p.y, from, to + L::NV * l.step);
+      if (has_y) l.fetch(p.y, from, to + L::NV * kSlot);
     }
     cp_async_commit();
   };
   if constexpr (RING) fetch(row, o, ring);
-  const uint32_t prod = smem_u32(s_mem) + t * 16;
   if (g.sub == 0) {
     f2 u[L::P], v[L::P];
     auto put = [&](int at) {
 #pragma unroll
-      for (int i = 0; i < kParam; ++i) sts128(prod + (at * kParam + i) * tpr * 16, narrow<4>(&v[2 * i]));
+      for (int i = 0; i < kParam; ++i) sts128(prod + (at * kParam + i) * kSlot, narrow<4>(&v[2 * i]));
     };
     l.param(p.gate != nullptr ? p.gate + b * p.gate_stride : nullptr, 1.f, v);
     l.param(p.post_gain, 1.f, u);
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid
     put(2);
   }
   __syncthreads();
-  auto product = [&](int at, int i, f2 (&m)[2]) { widen<4>(lds128(prod + (at * kParam + i) * tpr * 16), m); };
+  auto product = [&](int at, int i, f2 (&m)[2]) { widen<4>(lds128(prod + (at * kParam + i) * kSlot), m); };
   const f2 res = pack2(p.res_scale, p.res_scale);
   uint32_t now = ring, next = ring + slot_bytes;
   // a row of several warps stops by itself; rows that share a warp stop with the block's first
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid
     }
     if (has_y) {
       if (go) {
-        if constexpr (RING) l.take(now + L::NV * l.step, y);
+        if constexpr (RING) l.take(now + L::NV * kSlot, y);
         else l.load(p.y, o, y);
       }
       if (p.post_norm != NORM_NONE) scale_by(y, centre(l, g, y, p.post_norm, inv_c, p.eps));
@@ -423,9 +429,10 @@ __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const
   const bool has_y = f.y != nullptr, has_d = p.dx_out != nullptr;
   // slots: gain (1 + scale), gate post_gain, then the ring: x, dh, and y and dx_out where they are
   constexpr int kParam = E / 4;
-  const int tensors = 2 + has_y + has_d;
-  const L l{tpr, static_cast<int>(threadIdx.x) - g.sub * tpr, p.C, smem_u32(s_ring) + threadIdx.x * 16u, blockDim.x * 16u};
-  const uint32_t ring = l.slot(2 * kParam), slot_bytes = tensors * L::NV * l.step;
+  const L l(tpr, static_cast<int>(threadIdx.x) - g.sub * tpr, p.C,
+            smem_u32(s_ring) + threadIdx.x / 32 * (2 * kParam + (RING ? 8 * L::NV : 0)) * kSlot + threadIdx.x % 32 * 16);
+  const uint32_t ring = l.slot(2 * kParam);
+  constexpr uint32_t slot_bytes = 4 * L::NV * kSlot;
   const int stride = p.chunks * rpb;
   const size_t step = static_cast<size_t>(stride) * p.C * sizeof(T);
   int row = chunk * rpb + g.sub;
@@ -433,9 +440,9 @@ __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const
   auto fetch = [&](int r, size_t from, uint32_t to) {
     if (r < f.T) {
       l.fetch(f.x, from, to);
-      l.fetch(p.dh, from, to + L::NV * l.step);
-      if (has_y) l.fetch(f.y, from, to + 2 * L::NV * l.step);
-      if (has_d) l.fetch(p.dx_out, from, to + 3 * L::NV * l.step);  // only with y
+      l.fetch(p.dh, from, to + L::NV * kSlot);
+      if (has_y) l.fetch(f.y, from, to + 2 * L::NV * kSlot);
+      if (has_d) l.fetch(p.dx_out, from, to + 3 * L::NV * kSlot);  // only with y
     }
     cp_async_commit();
   };
@@ -483,7 +490,7 @@ __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const
       cp_async_wait<1>();
     }
     auto read = [&](int tensor, const void* from, f2 (&v)[L::P]) {
-      if constexpr (RING) l.take(now + tensor * L::NV * l.step, v);
+      if constexpr (RING) l.take(now + tensor * L::NV * kSlot, v);
       else l.load(from, o, v);
     };
     if (live) read(0, f.x, x);
@@ -670,8 +677,8 @@ template <typename T, int V, int E, bool RING, bool FULL, int MAXT>
 cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t stream) {
   // rows side by side in a block: as many as share an SM, unless the batch entries have fewer
   const long long share = (static_cast<long long>(a.B) * a.T + num_sms - 1) / num_sms;
-  const size_t row = static_cast<size_t>(s.tpr) * E * sizeof(T) * (a.y != nullptr ? 2 : 1) * (RING ? 2 : 0);
-  const size_t products = static_cast<size_t>(s.tpr) * E * 12;
+  const size_t row = RING ? static_cast<size_t>(s.tpr) * E * sizeof(T) * 4 : 0;  // two rows of x and y
+  const size_t products = static_cast<size_t>(s.tpr < 32 ? 32 : s.tpr) * E * 12;
   s.rpb = MAXT / s.tpr;
   if (s.tpr > 32 && s.rpb > 15) s.rpb = 15;
   if constexpr (RING) {
@@ -699,8 +706,8 @@ cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t s
 template <typename T, int V, bool FULL>
 cudaError_t launch_fwd(const NormArgs& a, const Shape& s, int num_sms, cudaStream_t stream) {
   if constexpr (V > 1) {
-    // two rows in the ring; fp32 rows of more than 7680 channels with a branch leave it no room and are read directly
-    if (static_cast<size_t>(s.tpr) * s.elems * (12 + 2 * sizeof(T) * (a.y != nullptr ? 2 : 1)) <= kSmemMax - 10240)
+    // two rows in the ring; fp32 rows of more than 7680 channels leave it no room and are read directly
+    if (static_cast<size_t>(s.tpr) * s.elems * (12 + 4 * sizeof(T)) <= kSmemMax - 10240)
       return s.elems == 8 ? launch_fwd_k<T, V, 8, true, FULL, 1024>(a, s, num_sms, stream)
                           : launch_fwd_k<T, V, 16, true, FULL, 1024>(a, s, num_sms, stream);
   }
@@ -709,8 +716,8 @@ cudaError_t launch_fwd(const NormArgs& a, const Shape& s, int num_sms, cudaStrea
 }
 
 template <typename T, int V, int E, bool RING, bool FULL, int MAXT, int MINB>
-cudaError_t launch_bwd_k(const NormBwdArgs& a, const Shape& s, int tensors, cudaStream_t stream) {
-  size_t smem = row_bytes(s, 8 + (RING ? 2 : 0) * tensors * static_cast<int>(sizeof(T)));
+cudaError_t launch_bwd_k(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
+  size_t smem = row_bytes(s, 8 + (RING ? 8 : 0) * static_cast<int>(sizeof(T)));
   if (s.rpb > 1 && smem < 12u * a.C) smem = 12u * a.C;  // the sums of a block's rows take the slots' place
   if (smem > 36 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(sol_residual_norm_bwd_kernel<T, V, E, RING, FULL, MAXT, MINB>,
@@ -721,22 +728,21 @@ cudaError_t launch_bwd_k(const NormBwdArgs& a, const Shape& s, int tensors, cuda
   return cudaGetLastError();
 }
 template <typename T, int V, int E, bool RING, bool FULL>
-cudaError_t launch_bwd_t(const NormBwdArgs& a, const Shape& s, int tensors, cudaStream_t stream) {
-  if constexpr (E == 8) return launch_bwd_k<T, V, E, RING, FULL, 256, 3>(a, s, tensors, stream);
-  else if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 2>(a, s, tensors, stream);
-  else return launch_bwd_k<T, V, E, RING, FULL, 512, 1>(a, s, tensors, stream);
+cudaError_t launch_bwd_t(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
+  if constexpr (E == 8) return launch_bwd_k<T, V, E, RING, FULL, 256, 3>(a, s, stream);
+  else if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 2>(a, s, stream);
+  else return launch_bwd_k<T, V, E, RING, FULL, 512, 1>(a, s, stream);
 }
 template <typename T, int V, bool FULL>
 cudaError_t launch_bwd(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
-  const int tensors = 2 + (a.fwd.y != nullptr) + (a.dx_out != nullptr);
   if constexpr (V > 1) {
     // two rows in the ring where they fit; fp32 rows of more than 5632 channels are read directly
-    if (row_bytes(s, 8 + 2 * tensors * static_cast<int>(sizeof(T))) <= kSmemMax - 8192)
-      return s.elems == 8 ? launch_bwd_t<T, V, 8, true, FULL>(a, s, tensors, stream)
-                          : launch_bwd_t<T, V, 16, true, FULL>(a, s, tensors, stream);
+    if (row_bytes(s, 8 + 8 * static_cast<int>(sizeof(T))) <= kSmemMax - 8192)
+      return s.elems == 8 ? launch_bwd_t<T, V, 8, true, FULL>(a, s, stream)
+                          : launch_bwd_t<T, V, 16, true, FULL>(a, s, stream);
   }
-  return s.elems == 8 ? launch_bwd_t<T, V, 8, false, FULL>(a, s, tensors, stream)
-                      : launch_bwd_t<T, V, 16, false, FULL>(a, s, tensors, stream);
+  return s.elems == 8 ? launch_bwd_t<T, V, 8, false, FULL>(a, s, stream)
+                      : launch_bwd_t<T, V, 16, false, FULL>(a, s, stream);
 }
 
 }  // namespace
