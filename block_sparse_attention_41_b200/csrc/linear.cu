@@ -30,6 +30,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "chained.cuh"
 #include "device_common.cuh"
 #include "launchers.h"
 
@@ -356,6 +357,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   pair_sync<CG>();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  chained_wait();
   const int units = unit_count(p), first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == 0) {
@@ -578,6 +580,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // without an epilogue (the gradients) are split.
 template <int CG, int TN>
 __global__ void __launch_bounds__(256) sol_linear_pieces_kernel(const __grid_constant__ GemmParams p, __nv_bfloat16* out) {
+  chained_wait();
   const int lane = threadIdx.x & 31, i = blockIdx.x * 8 + (threadIdx.x >> 5);
   constexpr int kChunks = CG * 4 * (TN / 32);
   const int tile = i / kChunks, in = i - tile * kChunks;
@@ -670,6 +673,7 @@ __global__ void __launch_bounds__(kFewThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  chained_wait();
 
   bool ok = true;  // of the epilogue warps: the accumulator is complete
   if (warp == 0) {
@@ -807,6 +811,7 @@ struct DzParams {
 template <int ACT>
 __global__ void __launch_bounds__(kDzCols / 8 * kDzRows) sol_linear_dz_kernel(const __grid_constant__ DzParams p) {
   __shared__ float s[kDzRows][kDzCols + 8];
+  chained_wait();
   const int lane = threadIdx.x, ty = threadIdx.y;
   const int c = blockIdx.x * kDzCols + lane * 8;
   const int r_lo = blockIdx.y * p.rows, r_hi = min(r_lo + p.rows, p.M);
@@ -852,6 +857,7 @@ __global__ void __launch_bounds__(kDzCols / 8 * kDzRows) sol_linear_dz_kernel(co
 __global__ void __launch_bounds__(512) sol_linear_db_kernel(const float* __restrict__ part, float* __restrict__ db, int N,
                                                             int chunks) {
   __shared__ float s[16][33];
+  chained_wait();
   const int col = blockIdx.x * 32 + threadIdx.x;
   float a = 0.f;
   if (col < N) {
@@ -896,24 +902,13 @@ cudaError_t launch_gemm_t(const GemmArgs& a, GemmParams p, cudaStream_t stream) 
   const int rest = static_cast<int>(tiles % units);
   p.split = a.tile.split;
   p.whole = static_cast<int>(tiles) - (p.split > 1 ? rest : 0);
-  cudaLaunchConfig_t cfg = {};
   const long long work = p.whole + static_cast<long long>(rest) * (p.split > 1 ? p.split : 0);
-  cfg.gridDim = dim3(CG * static_cast<int>(work < units ? work : units));
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
-  const cudaError_t le = cudaLaunchKernelEx(&cfg, sol_linear_kernel<CG, TN, A_MN, B_MN>, a.maps[0], a.maps[1], a.maps[2],
-                                            a.maps[3], a.maps[4], p);
+  const cudaError_t le = launch_chained(sol_linear_kernel<CG, TN, A_MN, B_MN>, dim3(CG * static_cast<int>(work < units ? work : units)),
+                                        dim3(kGemmThreads), C::SMEM, stream, CG, a.maps[0], a.maps[1], a.maps[2], a.maps[3],
+                                        a.maps[4], p);
   if (le != cudaSuccess || p.split == 1) return le;
-  sol_linear_pieces_kernel<CG, TN><<<rest * CG * 4 * (TN / 32) / 8, 256, 0, stream>>>(p, static_cast<__nv_bfloat16*>(a.out));
-  return cudaGetLastError();
+  return launch_chained(sol_linear_pieces_kernel<CG, TN>, dim3(rest * CG * 4 * (TN / 32) / 8), dim3(256), 0, stream, 1, p,
+                        static_cast<__nv_bfloat16*>(a.out));
 }
 
 template <bool A_MN, bool B_MN>
@@ -928,19 +923,8 @@ cudaError_t launch_few_t(const FewArgs& a, const FewParams& p, cudaStream_t stre
   using C = FewCfg<TT>;
   const cudaError_t e = allow_smem<sol_linear_few_kernel<TT>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.N + BM - 1) / BM * p.split);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, sol_linear_few_kernel<TT>, a.maps[0], a.maps[1], p);
+  return launch_chained(sol_linear_few_kernel<TT>, dim3((a.N + BM - 1) / BM * p.split), dim3(kFewThreads), C::SMEM, stream, p.split,
+                        a.maps[0], a.maps[1], p);
 }
 
 }  // namespace
@@ -1035,16 +1019,15 @@ cudaError_t launch_linear_dz(const void* dy, const void* z, int act, int M, int 
   const int chunks = linear_dz_chunks(M, N);
   p.rows = (M + chunks - 1) / chunks;
   const dim3 grid((N + kDzCols - 1) / kDzCols, chunks), block(kDzCols / 8, kDzRows);
+  cudaError_t e;
   switch (act) {
-    case ACT_GELU: sol_linear_dz_kernel<ACT_GELU><<<grid, block, 0, stream>>>(p); break;
-    case ACT_GELU_TANH: sol_linear_dz_kernel<ACT_GELU_TANH><<<grid, block, 0, stream>>>(p); break;
-    case ACT_SILU: sol_linear_dz_kernel<ACT_SILU><<<grid, block, 0, stream>>>(p); break;
-    default: sol_linear_dz_kernel<ACT_NONE><<<grid, block, 0, stream>>>(p); break;
+    case ACT_GELU: e = launch_chained(sol_linear_dz_kernel<ACT_GELU>, grid, block, 0, stream, 1, p); break;
+    case ACT_GELU_TANH: e = launch_chained(sol_linear_dz_kernel<ACT_GELU_TANH>, grid, block, 0, stream, 1, p); break;
+    case ACT_SILU: e = launch_chained(sol_linear_dz_kernel<ACT_SILU>, grid, block, 0, stream, 1, p); break;
+    default: e = launch_chained(sol_linear_dz_kernel<ACT_NONE>, grid, block, 0, stream, 1, p); break;
   }
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || part == nullptr) return e;
-  sol_linear_db_kernel<<<(N + 31) / 32, dim3(32, 16), 0, stream>>>(part, db, N, chunks);
-  return cudaGetLastError();
+  return launch_chained(sol_linear_db_kernel, dim3((N + 31) / 32), dim3(32, 16), 0, stream, 1, part, db, N, chunks);
 }
 
 }  // namespace sol

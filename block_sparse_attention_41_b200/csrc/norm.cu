@@ -17,6 +17,7 @@
 // instruction; only the stored rows are rounded.
 #include <cmath>
 
+#include "chained.cuh"
 #include "device_common.cuh"
 #include "launchers.h"
 
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid
     }
     cp_async_commit();
   };
+  chained_wait();
   if constexpr (RING) fetch(row, o, ring);
   if (g.sub == 0) {
     f2 u[L::P], v[L::P];
@@ -446,6 +448,7 @@ __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const
     }
     cp_async_commit();
   };
+  chained_wait();
   if constexpr (RING) fetch(row, o, ring);
   f2 aP[L::P], aS[L::P], aQ[L::P];
   {
@@ -607,6 +610,7 @@ __device__ __forceinline__ float column_sum(F&& get, int n) {
 // Latency is what counts, so the three sums and the slots go to as many threads as there are.
 __global__ void __launch_bounds__(kSumCols* kSumRows) sol_residual_norm_sum_kernel(const __grid_constant__ NormBwdArgs p,
                                                                                   int slots) {
+  chained_wait();
   const int b = blockIdx.y, which = blockIdx.z, cc = blockIdx.x * kSumCols + threadIdx.x;
   const bool on = cc < p.C;
   const int c = on ? cc : 0;
@@ -635,6 +639,7 @@ __global__ void __launch_bounds__(kSumCols* kSumRows) sol_residual_norm_sum_kern
 // The shared gains' gradients: the batch entries' shares added.
 __global__ void __launch_bounds__(kSumCols* kSumRows) sol_residual_norm_sum_b_kernel(const __grid_constant__ NormBwdArgs p,
                                                                                     int slots) {
+  chained_wait();
   const int cc = blockIdx.x * kSumCols + threadIdx.x;
   const bool on = cc < p.C;
   const int c = on ? cc : 0;
@@ -699,9 +704,8 @@ cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t s
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  sol_residual_norm_kernel<T, V, E, RING, FULL, MAXT>
-      <<<static_cast<unsigned>(a.B * chunks), s.threads, smem, stream>>>(a, s.tpr, static_cast<int>(chunks));
-  return cudaGetLastError();
+  return launch_chained(sol_residual_norm_kernel<T, V, E, RING, FULL, MAXT>, dim3(static_cast<unsigned>(a.B * chunks)),
+                        dim3(s.threads), smem, stream, 1, a, s.tpr, static_cast<int>(chunks));
 }
 template <typename T, int V, bool FULL>
 cudaError_t launch_fwd(const NormArgs& a, const Shape& s, int num_sms, cudaStream_t stream) {
@@ -724,8 +728,8 @@ cudaError_t launch_bwd_k(const NormBwdArgs& a, const Shape& s, cudaStream_t stre
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  sol_residual_norm_bwd_kernel<T, V, E, RING, FULL, MAXT, MINB><<<a.fwd.B * a.chunks, s.threads, smem, stream>>>(a, s.tpr);
-  return cudaGetLastError();
+  return launch_chained(sol_residual_norm_bwd_kernel<T, V, E, RING, FULL, MAXT, MINB>, dim3(a.fwd.B * a.chunks), dim3(s.threads),
+                        smem, stream, 1, a, s.tpr);
 }
 template <typename T, int V, int E, bool RING, bool FULL>
 cudaError_t launch_bwd_t(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
@@ -783,11 +787,9 @@ cudaError_t launch_residual_norm_bwd(const NormBwdArgs& a, cudaStream_t stream) 
   const int slots = a.chunks;
   const dim3 block(kSumCols, kSumRows);
   const unsigned cols = (a.C + kSumCols - 1) / kSumCols;
-  sol_residual_norm_sum_kernel<<<dim3(cols, f.B, 3), block, 0, stream>>>(a, slots);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_chained(sol_residual_norm_sum_kernel, dim3(cols, f.B, 3), block, 0, stream, 1, a, slots)) != cudaSuccess) return e;
   if (f.B > 1 && (a.dgain != nullptr || a.dpost_gain != nullptr)) {
-    sol_residual_norm_sum_b_kernel<<<cols, block, 0, stream>>>(a, slots);
-    e = cudaGetLastError();
+    e = launch_chained(sol_residual_norm_sum_b_kernel, dim3(cols), block, 0, stream, 1, a, slots);
   }
   return e;
 }

@@ -17,6 +17,7 @@
 // strides of their own: the same pass takes a token-major projection to head-major rows, or back.
 #include <cmath>
 
+#include "chained.cuh"
 #include "device_common.cuh"
 #include "launchers.h"
 
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kThreads) sol_rope_interleaved_kernel(const __
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int t = static_cast<int>(i / groups), g = static_cast<int>(i - static_cast<long long>(t) * groups);
   if (t >= p.L) return;
+  chained_wait();
   const int b = blockIdx.z, col = g * V;
   const int heads = p.side[0].heads + p.side[1].heads;
   const int h0 = blockIdx.y * heads_per_block, h1 = min(h0 + heads_per_block, heads);
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 8) sol_rope_half_kernel(const __grid
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int t = static_cast<int>(i / groups), g = static_cast<int>(i - static_cast<long long>(t) * groups);
   if (t >= p.L) return;
+  chained_wait();
   const int b = blockIdx.z, half = p.rot / 2;
   const int heads = p.side[0].heads + p.side[1].heads;
   const int h0 = blockIdx.y * heads_per_block, h1 = min(h0 + heads_per_block, heads);
@@ -279,9 +282,8 @@ cudaError_t launch_t(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   int hpb = static_cast<int>((heads + split - 1) / split);
   if (hpb < 4) hpb = heads < 4 ? heads : 4;
   const dim3 grid(static_cast<unsigned>(blocks), (heads + hpb - 1) / hpb, a.B);
-  if (a.half) sol_rope_half_kernel<T, V><<<grid, kThreads, 0, stream>>>(a, groups, hpb);
-  else sol_rope_interleaved_kernel<T, VI><<<grid, kThreads, 0, stream>>>(a, groups, hpb);
-  return cudaGetLastError();
+  return launch_chained(a.half ? sol_rope_half_kernel<T, V> : sol_rope_interleaved_kernel<T, VI>, grid, dim3(kThreads), 0, stream, 1,
+                        a, groups, hpb);
 }
 
 // Tables: V pairs of one token per thread and turn of the loop, the same pairs every time, so that
@@ -290,6 +292,7 @@ template <int V>
 __global__ void __launch_bounds__(kTableThreads) sol_rope_tables_kernel(const __grid_constant__ RopeTableArgs p, int groups, int tokens,
                                                                     int share) {
   const int half = p.rot / 2, g = threadIdx.x % groups;
+  chained_wait();
   if (threadIdx.x >= groups * tokens) return;
   // a block's tokens lie together: their positions share cache lines
   const long long from = static_cast<long long>(blockIdx.x) * share;
@@ -356,9 +359,8 @@ cudaError_t launch_rope_tables(const RopeTableArgs& a, int num_sms, cudaStream_t
   const long long turns = (static_cast<long long>(a.L) + tokens - 1) / tokens, per = (turns + 4ll * num_sms - 1) / (4ll * num_sms);
   const unsigned grid = static_cast<unsigned>((turns + per - 1) / per);
   const int share = static_cast<int>(per * tokens);
-  if (vec) sol_rope_tables_kernel<4><<<grid, kTableThreads, 0, stream>>>(a, groups, tokens, share);
-  else sol_rope_tables_kernel<1><<<grid, kTableThreads, 0, stream>>>(a, groups, tokens, share);
-  return cudaGetLastError();
+  return launch_chained(vec ? sol_rope_tables_kernel<4> : sol_rope_tables_kernel<1>, dim3(grid), dim3(kTableThreads), 0, stream, 1, a,
+                        groups, tokens, share);
 }
 
 }  // namespace sol
