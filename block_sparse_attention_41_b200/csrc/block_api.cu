@@ -220,7 +220,7 @@ sol_status sol_attn_residual_norm_bwd(const void* dh, const void* dx_out, const 
   a.dpost_gain = dpost_gain;
   a.part = any ? static_cast<float*>(workspace) : nullptr;
   a.C = C;
-  a.chunks = sol::norm_bwd_chunks(B, T, C);
+  a.chunks = sol::norm_bwd_chunks(B, T, C, a.fwd.vec);
   const cudaError_t e = sol::launch_residual_norm_bwd(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "residual norm gradient launch");
   return SOL_OK;

@@ -147,10 +147,10 @@ struct NormBwdArgs {
   float* dgain;        // [C] or null
   float* dpost_gain;   // [C] or null
   float* part;         // workspace of norm_bwd_part_floats, or null where no vector's gradient is wanted
-  int C, chunks;       // chunks = norm_bwd_chunks(B, T, C)
+  int C, chunks;       // chunks = norm_bwd_chunks(B, T, C, fwd.vec)
 };
 constexpr int kNormBwdBlocks = 592;  // 4 per SM, of which 1 to 3 are taken over all batch entries
-int norm_bwd_chunks(int B, int T, int C);
+int norm_bwd_chunks(int B, int T, int C, bool vec);
 size_t norm_bwd_part_floats(int B, int T, int C);
 cudaError_t launch_residual_norm_bwd(const NormBwdArgs& a, cudaStream_t stream);
 

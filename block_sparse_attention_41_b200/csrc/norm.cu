@@ -16,6 +16,7 @@
 // moments, so a large common offset costs no digits. All arithmetic is fp32, two channels per
 // instruction; only the stored rows are rounded.
 #include <cmath>
+#include <type_traits>
 
 #include "chained.cuh"
 #include "device_common.cuh"
@@ -25,7 +26,7 @@ namespace sol {
 
 namespace {
 
-constexpr int kMaxWarps = 16;  // of a row
+constexpr int kMaxWarps = 32;  // of a row
 constexpr int kSlot = 512;     // 16 bytes of each of a warp's threads
 constexpr int kMaxRows = 16;   // of several warps in a block: 15 named barriers
 constexpr int kSmemMax = 227 * 1024;  // per block
@@ -85,11 +86,12 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
 // A warp's channels lie together, so that a thread's vectors and slots are at fixed distances: rows
 // are addressed by the byte offset of the thread's first channel, which the loops carry along, and
 // everything else is an immediate (address arithmetic was a third of the instructions before).
-// FULL: every vector lies within the row, and a row has whole warps.
+// FULL: every vector of the warp lies within the row, and a row has whole warps.
 template <typename T, int V, int E, bool FULL>
 struct Lane {
-  static constexpr int NV = E / V, P = E / 2;
+  enum : int { NV = E / V, P = E / 2 };  // vectors, pairs
   static constexpr bool kFull = FULL;
+  static constexpr int kMost = V == 1 ? kMaxWarps : 16;  // warps of a row: single values may be 8 to a thread
   int first, side, C;  // first channel; threads side by side (32, or a shorter row's)
   uint32_t smem;
 
@@ -207,8 +209,8 @@ __device__ __forceinline__ RowGroup row_group(float* s_buf, int tpr) {
 
 // Sums of N values over a row, the same for all its threads. Each thread adds the warps' sums itself:
 // a few 16-byte broadcasts take a third of the latency of five more shuffles.
-// WARPS: a row has whole warps.
-template <bool WARPS, int N>
+// WARPS: a row has whole warps; MOST: how many at most.
+template <bool WARPS, int MOST, int N>
 __device__ __forceinline__ void row_sum(RowGroup& g, float (&v)[N]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -234,6 +236,9 @@ __device__ __forceinline__ void row_sum(RowGroup& g, float (&v)[N]) {
       const float4 d = q[2], e = q[3];
       s += ((d.x + d.y) + (d.z + d.w)) + ((e.x + e.y) + (e.z + e.w));
     }
+    if constexpr (MOST > 16) {
+      for (int k = 4; 4 * k < g.nwarps; ++k) s += (q[k].x + q[k].y) + (q[k].z + q[k].w);
+    }
     v[i] = s;
   }
 }
@@ -247,7 +252,7 @@ __device__ __forceinline__ float centre(const L& l, RowGroup& g, f2 (&x)[L::P], 
 #pragma unroll
     for (int i = 1; i < L::P; ++i) s = add2(s, x[i]);
     float v[1] = {sum2(s)};
-    row_sum<L::kFull>(g, v);
+    row_sum<L::kFull, L::kMost>(g, v);
     const f2 m = pack2(-v[0] * inv_c, -v[0] * inv_c);
 #pragma unroll
     for (int i = 0; i < L::P; ++i) x[i] = add2(x[i], m);
@@ -257,7 +262,7 @@ __device__ __forceinline__ float centre(const L& l, RowGroup& g, f2 (&x)[L::P], 
 #pragma unroll
   for (int i = 1; i < L::P; ++i) q = fma2(x[i], x[i], q);
   float v[1] = {sum2(q)};
-  row_sum<L::kFull>(g, v);
+  row_sum<L::kFull, L::kMost>(g, v);
   return 1.0f / sqrtf(fmaf(v[0], inv_c, eps));
 }
 template <int P>
@@ -282,12 +287,12 @@ __device__ __forceinline__ void normalise_back(const L& l, RowGroup& g, f2 (&w)[
 #pragma unroll
     for (int i = 1; i < L::P; ++i) m = add2(m, w[i]);
     float v[2] = {sum2(s), sum2(m)};
-    row_sum<L::kFull>(g, v);
+    row_sum<L::kFull, L::kMost>(g, v);
     a = -v[0] * inv_c * r;
     m = pack2(-v[1] * inv_c, -v[1] * inv_c);
   } else {
     float v[1] = {sum2(s)};
-    row_sum<L::kFull>(g, v);
+    row_sum<L::kFull, L::kMost>(g, v);
     a = -v[0] * inv_c * r;
   }
   const f2 rr = pack2(r, r), aa = pack2(a, a);
@@ -431,15 +436,16 @@ __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const
   const bool has_y = f.y != nullptr, has_d = p.dx_out != nullptr;
   // slots: gain (1 + scale), gate post_gain, then the ring: x, dh, and y and dx_out where they are
   constexpr int kParam = E / 4;
-  const L l(tpr, static_cast<int>(threadIdx.x) - g.sub * tpr, p.C,
-            smem_u32(s_ring) + threadIdx.x / 32 * (2 * kParam + (RING ? 8 * L::NV : 0)) * kSlot + threadIdx.x % 32 * 16);
+  const int t = static_cast<int>(threadIdx.x) - g.sub * tpr;
+  const uint32_t mem = smem_u32(s_ring) + threadIdx.x / 32 * (2 * kParam + (RING ? 8 * L::NV : 0)) * kSlot + threadIdx.x % 32 * 16;
+  const L l(tpr, t, p.C, mem);
   const uint32_t ring = l.slot(2 * kParam);
   constexpr uint32_t slot_bytes = 4 * L::NV * kSlot;
   const int stride = p.chunks * rpb;
   const size_t step = static_cast<size_t>(stride) * p.C * sizeof(T);
   int row = chunk * rpb + g.sub;
   size_t o = (static_cast<size_t>(b) * f.T + row) * p.C * sizeof(T) + static_cast<size_t>(l.chan(0)) * sizeof(T);
-  auto fetch = [&](int r, size_t from, uint32_t to) {
+  auto fetch = [&](const auto& l, int r, size_t from, uint32_t to) {
     if (r < f.T) {
       l.fetch(f.x, from, to);
       l.fetch(p.dh, from, to + L::NV * kSlot);
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const
     cp_async_commit();
   };
   chained_wait();
-  if constexpr (RING) fetch(row, o, ring);
+  if constexpr (RING) fetch(l, row, o, ring);
   f2 aP[L::P], aS[L::P], aQ[L::P];
   {
     f2 u[L::P], v[L::P];
@@ -481,73 +487,79 @@ __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const
   const f2 res = pack2(f.res_scale, f.res_scale);
   __syncthreads();  // the exchange buffer is zeroed
   uint32_t now = ring, next = ring + slot_bytes;
-  for (int lead = FULL ? row : chunk * rpb; lead < f.T; lead += stride, row += stride, o += step) {
-    const bool live = FULL || row < f.T;
-    f2 x[L::P], y[L::P], w[L::P];
-    if constexpr (!FULL) {
+  auto rows = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    const Lane<T, V, E, kWhole> l(tpr, t, p.C, mem);
+    for (int lead = kWhole || tpr >= 32 ? row : chunk * rpb; lead < f.T; lead += stride, row += stride, o += step) {
+      const bool live = kWhole || row < f.T;
+      f2 x[L::P], y[L::P], w[L::P];
+      if constexpr (!kWhole) {
 #pragma unroll
-      for (int k = 0; k < L::P; ++k) x[k] = y[k] = w[k] = pack2(0.f, 0.f);
-    }
-    if constexpr (RING) {
-      fetch(row + stride, o + step, next);
-      cp_async_wait<1>();
-    }
-    auto read = [&](int tensor, const void* from, f2 (&v)[L::P]) {
-      if constexpr (RING) l.take(now + tensor * L::NV * kSlot, v);
-      else l.load(from, o, v);
-    };
-    if (live) read(0, f.x, x);
-    float ry = 0.f;
-    if (has_y) {
-      if (live) read(2, f.y, y);
-      if (f.post_norm != NORM_NONE) {
-        ry = centre(l, g, y, f.post_norm, inv_c, f.eps);
-        scale_by(y, ry);
+        for (int k = 0; k < L::P; ++k) x[k] = y[k] = w[k] = pack2(0.f, 0.f);
       }
-      times(y, kParam, w);
-#pragma unroll
-      for (int k = 0; k < L::P; ++k) x[k] = fma2(res, x[k], w[k]);
-    }
-    const float r = centre(l, g, x, f.norm, inv_c, f.eps);
-    scale_by(x, r);
-    if constexpr (!FULL) {
-#pragma unroll
-      for (int k = 0; k < L::P; ++k) w[k] = pack2(0.f, 0.f);
-    }
-    if (live) read(1, p.dh, w);
-#pragma unroll
-    for (int k = 0; k < L::P; ++k) {
-      aP[k] = fma2(w[k], x[k], aP[k]);
-      aS[k] = add2(aS[k], w[k]);
-    }
-    times(w, 0, w);
-    normalise_back(l, g, w, x, r, f.norm, inv_c);
-    if (has_d && live) {
-      f2 d[L::P];
-      if constexpr (!FULL) {
-#pragma unroll
-        for (int k = 0; k < L::P; ++k) d[k] = pack2(0.f, 0.f);
+      if constexpr (RING) {
+        fetch(l, row + stride, o + step, next);
+        cp_async_wait<1>();
       }
-      read(3, p.dx_out, d);
+      auto read = [&](int tensor, const void* from, f2 (&v)[L::P]) {
+        if constexpr (RING) l.take(now + tensor * L::NV * kSlot, v);
+        else l.load(from, o, v);
+      };
+      if (live) read(0, f.x, x);
+      float ry = 0.f;
+      if (has_y) {
+        if (live) read(2, f.y, y);
+        if (f.post_norm != NORM_NONE) {
+          ry = centre(l, g, y, f.post_norm, inv_c, f.eps);
+          scale_by(y, ry);
+        }
+        times(y, kParam, w);
 #pragma unroll
-      for (int k = 0; k < L::P; ++k) w[k] = add2(w[k], d[k]);
+        for (int k = 0; k < L::P; ++k) x[k] = fma2(res, x[k], w[k]);
+      }
+      const float r = centre(l, g, x, f.norm, inv_c, f.eps);
+      scale_by(x, r);
+      if constexpr (!kWhole) {
+#pragma unroll
+        for (int k = 0; k < L::P; ++k) w[k] = pack2(0.f, 0.f);
+      }
+      if (live) read(1, p.dh, w);
+#pragma unroll
+      for (int k = 0; k < L::P; ++k) {
+        aP[k] = fma2(w[k], x[k], aP[k]);
+        aS[k] = add2(aS[k], w[k]);
+      }
+      times(w, 0, w);
+      normalise_back(l, g, w, x, r, f.norm, inv_c);
+      if (has_d && live) {
+        f2 d[L::P];
+        if constexpr (!kWhole) {
+#pragma unroll
+          for (int k = 0; k < L::P; ++k) d[k] = pack2(0.f, 0.f);
+        }
+        read(3, p.dx_out, d);
+#pragma unroll
+        for (int k = 0; k < L::P; ++k) w[k] = add2(w[k], d[k]);
+      }
+      if (has_y) {
+#pragma unroll
+        for (int k = 0; k < L::P; ++k) x[k] = mul2(w[k], res);
+        if (live) l.store(p.dx, o, x);
+#pragma unroll
+        for (int k = 0; k < L::P; ++k) aQ[k] = fma2(w[k], y[k], aQ[k]);
+        times(w, kParam, w);
+        if (f.post_norm != NORM_NONE) normalise_back(l, g, w, y, ry, f.post_norm, inv_c);
+        if (live) l.store(p.dy, o, w);
+      } else if (live) {
+        l.store(p.dx, o, w);
+      }
+      const uint32_t free = now;
+      now = next;
+      next = free;
     }
-    if (has_y) {
-#pragma unroll
-      for (int k = 0; k < L::P; ++k) x[k] = mul2(w[k], res);
-      if (live) l.store(p.dx, o, x);
-#pragma unroll
-      for (int k = 0; k < L::P; ++k) aQ[k] = fma2(w[k], y[k], aQ[k]);
-      times(w, kParam, w);
-      if (f.post_norm != NORM_NONE) normalise_back(l, g, w, y, ry, f.post_norm, inv_c);
-      if (live) l.store(p.dy, o, w);
-    } else if (live) {
-      l.store(p.dx, o, w);
-    }
-    const uint32_t free = now;
-    now = next;
-    next = free;
-  }
+  };
+  if (FULL || (tpr >= 32 && (t / 32 + 1) * 32 * E <= p.C)) rows(std::true_type{});
+  else if constexpr (!FULL) rows(std::false_type{});
   if constexpr (RING) cp_async_wait<0>();
   if (p.part == nullptr) return;
   // a row past the end added zeros only; rows side by side: first those of a warp, then warp by warp
@@ -655,27 +667,32 @@ __global__ void __launch_bounds__(kSumCols* kSumRows) sol_residual_norm_sum_b_ke
   }
 }
 
-// How a row is laid over threads: the channels per thread that pad a row least, at a tie the larger,
-// which halves the shuffles per value; rows of more than 2048 channels always take 16, since a
-// block of 8-channel threads would not leave them registers enough.
+// How a row is laid over threads, `elems` channels each.
 struct Shape {
   int elems, tpr, rpb, threads;
 };
-Shape shape_of(int C) {
-  auto per_row = [C](int e) {
-    const int n = (C + e - 1) / e;
-    if (n >= 32) return (n + 31) / 32 * 32;
-    int t = 1;
-    while (t < n) t *= 2;
-    return t;
-  };
+Shape shape_of(int C, int elems) {
   Shape s;
-  s.elems = C > 2048 || 16 * per_row(16) <= 8 * per_row(8) ? 16 : 8;
-  s.tpr = per_row(s.elems);
+  s.elems = elems;
+  const int n = (C + elems - 1) / elems;
+  if (n >= 32) {
+    s.tpr = (n + 31) / 32 * 32;
+  } else {
+    s.tpr = 1;
+    while (s.tpr < n) s.tpr *= 2;
+  }
   s.rpb = s.tpr >= 256 ? 1 : 256 / s.tpr;
   s.threads = s.tpr * s.rpb;
   return s;
 }
+// 16 channels halve the shuffles per value (gradient of 20000 x 5120 bf16: 357 us in ten warps per SM, 434
+// in twenty with 8); 8 pad short rows less, and leave the gradient's single values room for an
+// address and a test each (20000 x 5119: 900 us, 1500 with 16 that spill).
+int fwd_elems(int C) {
+  const Shape a = shape_of(C, 16), b = shape_of(C, 8);
+  return C > 2048 || 16 * a.tpr <= 8 * b.tpr ? 16 : 8;
+}
+int bwd_elems(int C, bool vec) { return !vec && C <= 6144 ? 8 : fwd_elems(C); }
 size_t row_bytes(const Shape& s, int bytes) { return static_cast<size_t>(s.threads) * s.elems * bytes; }
 
 template <typename T, int V, int E, bool RING, bool FULL, int MAXT>
@@ -733,15 +750,18 @@ cudaError_t launch_bwd_k(const NormBwdArgs& a, const Shape& s, cudaStream_t stre
 }
 template <typename T, int V, int E, bool RING, bool FULL>
 cudaError_t launch_bwd_t(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
-  if constexpr (E == 8) return launch_bwd_k<T, V, E, RING, FULL, 256, 3>(a, s, stream);
-  else if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 2>(a, s, stream);
+  if constexpr (E == 8) {
+    if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 3>(a, s, stream);
+    if constexpr (V == 1) return launch_bwd_k<T, V, E, RING, FULL, 768, 1>(a, s, stream);
+    else return cudaErrorInvalidValue;  // bwd_elems gives 8 of these to 256 threads at most
+  } else if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 2>(a, s, stream);
   else return launch_bwd_k<T, V, E, RING, FULL, 512, 1>(a, s, stream);
 }
 template <typename T, int V, bool FULL>
 cudaError_t launch_bwd(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
   if constexpr (V > 1) {
-    // two rows in the ring where they fit; fp32 rows of more than 5632 channels are read directly
-    if (row_bytes(s, 8 + 8 * static_cast<int>(sizeof(T))) <= kSmemMax - 8192)
+    // two rows in the ring where they fit; fp32 rows of more than 5376 channels are read directly
+    if (row_bytes(s, 8 + 8 * static_cast<int>(sizeof(T))) <= kSmemMax - 10240)
       return s.elems == 8 ? launch_bwd_t<T, V, 8, true, FULL>(a, s, stream)
                           : launch_bwd_t<T, V, 16, true, FULL>(a, s, stream);
   }
@@ -751,17 +771,21 @@ cudaError_t launch_bwd(const NormBwdArgs& a, const Shape& s, cudaStream_t stream
 
 }  // namespace
 
-int norm_bwd_chunks(int B, int T, int C) {
-  const Shape s = shape_of(C);
+int norm_bwd_chunks(int B, int T, int C, bool vec) {
+  // one to three blocks per SM, as many as fit
+  const Shape s = shape_of(C, bwd_elems(C, vec));
   const int most = (T + s.rpb - 1) / s.rpb;
   const int blocks = s.threads > 256 ? kNormBwdBlocks / 4 : s.elems == 16 ? kNormBwdBlocks / 2 : kNormBwdBlocks * 3 / 4;
   const int want = blocks / B > 1 ? blocks / B : 1;
   return most < want ? most : want;
 }
-size_t norm_bwd_part_floats(int B, int T, int C) { return static_cast<size_t>(B) * norm_bwd_chunks(B, T, C) * 3 * C; }
+size_t norm_bwd_part_floats(int B, int T, int C) {  // for either kind of access, which the sizes alone do not tell
+  const int a = norm_bwd_chunks(B, T, C, true), b = norm_bwd_chunks(B, T, C, false);
+  return static_cast<size_t>(B) * (a > b ? a : b) * 3 * C;
+}
 
 cudaError_t launch_residual_norm(const NormArgs& a, int num_sms, cudaStream_t stream) {
-  const Shape s = shape_of(a.C);
+  const Shape s = shape_of(a.C, fwd_elems(a.C));
   const bool full = a.C == s.tpr * s.elems && s.tpr >= 32;
   if (a.bf16) {
     if (!a.vec) return launch_fwd<__nv_bfloat16, 1, false>(a, s, num_sms, stream);
@@ -773,7 +797,7 @@ cudaError_t launch_residual_norm(const NormArgs& a, int num_sms, cudaStream_t st
 
 cudaError_t launch_residual_norm_bwd(const NormBwdArgs& a, cudaStream_t stream) {
   const NormArgs& f = a.fwd;
-  const Shape s = shape_of(a.C);
+  const Shape s = shape_of(a.C, bwd_elems(a.C, f.vec));
   const bool full = a.C == s.tpr * s.elems && s.tpr >= 32;
   cudaError_t e;
   if (f.bf16) {
