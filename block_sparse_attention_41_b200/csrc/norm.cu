@@ -701,15 +701,17 @@ cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t s
   const long long share = (static_cast<long long>(a.B) * a.T + num_sms - 1) / num_sms;
   const size_t row = RING ? static_cast<size_t>(s.tpr) * E * sizeof(T) * 4 : 0;  // two rows of x and y
   const size_t products = static_cast<size_t>(s.tpr < 32 ? 32 : s.tpr) * E * 12;
-  s.rpb = MAXT / s.tpr;
-  if (s.tpr > 32 && s.rpb > 15) s.rpb = 15;
+  const int unit = s.tpr < 32 ? 32 / s.tpr : 1;  // whole warps
+  long long rows = MAXT / s.tpr;
+  if (s.tpr > 32 && rows > 15) rows = 15;  // each with a named barrier
+  if (rows > a.T) rows = a.T;
+  if (rows > share) rows = share;
+  rows = (rows + unit - 1) / unit * unit;
   if constexpr (RING) {
-    const long long fit = static_cast<long long>((kSmemMax - 10240 - products) / row);
-    if (s.rpb > fit) s.rpb = static_cast<int>(fit);
+    const long long fit = static_cast<long long>((kSmemMax - 10240 - products) / row) / unit * unit;
+    if (rows > fit) rows = fit;
   }
-  if (s.rpb > a.T) s.rpb = a.T;
-  if (s.rpb > share) s.rpb = static_cast<int>(share);
-  if (s.tpr < 32) s.rpb = (s.rpb * s.tpr + 31) / 32 * 32 / s.tpr;  // whole warps
+  s.rpb = static_cast<int>(rows);
   s.threads = s.tpr * s.rpb;
   const size_t smem = products + row * s.rpb;
   const long long per_sm = static_cast<long long>(MAXT / s.threads) < 1 ? 1 : MAXT / s.threads;

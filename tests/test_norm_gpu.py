@@ -182,6 +182,25 @@ def test_rows_of_zeros_and_constants_give_the_shift():
     assert torch.equal(h[0, 0], a["shift"][0])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [1, 5, 8, 31, 72, 100, 128, 200, 256, 300, 511, 512, 1000, 1032])
+def test_many_rows_of_few_channels(C, dtype):
+    # full blocks: as many rows side by side as threads, barriers and shared memory allow
+    T = 30_000 if C <= 300 else 6000
+    a = make(2, T, C, dtype, post=True)
+    check_forward(a, dtype, "rms", "rms")
+    check_backward(make(1, T // 4, C, dtype, post=True), dtype, "layer", "rms")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [4104, 5376, 6144, 6145, 7680, 7684, 7688, 8184, 8191])
+def test_long_ragged_rows(C, dtype):
+    # around the sizes where the gradient or the forward changes its threads or leaves the ring out
+    a = make(1, 400, C, dtype, post=True)
+    check_forward(a, dtype, "layer", "layer")
+    check_backward(a, dtype, "rms", "rms")
+
+
 def test_a_large_common_offset_keeps_its_digits():
     # rows at 1000 with a deviation of 1: a difference of moments in fp32 would lose the variance's digits
     a = make(1, 6, 2048, "f32", y=False, offset=1000.0)
