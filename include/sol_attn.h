@@ -466,7 +466,8 @@ size_t sol_attn_linear_bwd_workspace_bytes(int M, int N, sol_activation act);
  *   dy         device, bf16 [M, N];  x, w as in the forward (NULL where only needed for a null output)
  *   z          device, bf16 [M, N] from the forward, exactly where act is not SOL_ACT_NONE
  *   dx         device, out, bf16 [M, K];  dw: bf16 [N, K];  db: float32 [N]; each NULL where not wanted
- *   workspace  device, sol_attn_linear_bwd_workspace_bytes(...) bytes; only its first 256 need zeroing,
+ *   workspace  device, sol_attn_linear_bwd_workspace_bytes(...) bytes (sums of db, pieces of split tiles,
+ *              and dz where there is an activation); only its first 256 need zeroing,
  *              and only for sol_attn_check_device_error */
 sol_status sol_attn_linear_bwd(const void* dy, const void* x, const void* w, const void* z,
                                sol_activation act, int M, int N, int K, void* dx, void* dw, float* db,
