@@ -385,13 +385,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_PRODUCER);
       // No copy may be in flight when shared memory is released: the last use of every slice. Rank 1 cannot
-      // see its own land: rank 0 does, before both meet at the end; after an abort it waits a while.
+      // see its own land, but every MMA that reads them has ended when the last commit arrives here, and with
+      // it every other commit to this CTA's barriers; after an abort it waits a while for the rest.
       if (rank == 0) {
         for (uint32_t i = g > C::NS ? g - C::NS : 0; i < g; ++i)
           mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, kWaitLimitNs);
-      } else if (w != WAIT_OK) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) {
+      } else {
+        mbar_wait(bar_drain, 0, nullptr, 2 * kWaitLimitNs);
+        if (w != WAIT_OK) {
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 1000000ull) {
+          }
         }
       }
     }
