@@ -116,8 +116,8 @@ sol_status make_operand_map(CUtensorMap* m, const void* base, int rows, int inne
 // [Ko, Mo]; B as [No, Ko] or, b_mn, as [Ko, No].
 sol_status run_gemm(sol::GemmArgs& a, const void* A, const void* Bm, void* out, void* z, cudaStream_t stream) {
   a.tile = sol::linear_tile(a.Mo, a.No, a.Ko, a.part != nullptr, a.num_sms);
-  a.store_z = z != nullptr;
   a.out = out;
+  a.z = z;
   sol_status st;
   if ((st = make_operand_map(&a.maps[0], A, a.a_mn ? a.Ko : a.Mo, a.a_mn ? a.Mo : a.Ko, a.a_mn, 128)) != SOL_OK) return st;
   if ((st = make_operand_map(&a.maps[1], Bm, a.b_mn ? a.Ko : a.No, a.b_mn ? a.No : a.Ko, a.b_mn, a.tile.n / a.tile.ctas)) != SOL_OK) return st;
@@ -362,6 +362,15 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
   return SOL_OK;
 }
 
+size_t sol_attn_linear_workspace_bytes(int M, int N, int K) {
+  if (linear_sizes(M, N, K, SOL_ACT_NONE) != SOL_OK) {
+    clear_error();
+    return 0;
+  }
+  const bool split = M > sol::kFewRows && sol::linear_tile(M, N, K, true, kMaxSms).split > 1;
+  return kErrorBytes + (split ? sol::linear_part_bytes(kMaxSms) : 0);
+}
+
 sol_status sol_attn_linear(const void* x, const void* w, const float* bias, const void* residual, sol_activation act, int M,
                            int N, int K, void* out, void* z, void* workspace, size_t ws_bytes, void* stream) {
   clear_error();
@@ -400,7 +409,9 @@ sol_status sol_attn_linear(const void* x, const void* w, const float* bias, cons
   a.bias = bias;
   a.residual = residual;
   a.act = act;
-  a.part = nullptr;
+  a.part = workspace != nullptr && ws_bytes >= kErrorBytes + sol::linear_part_bytes(kMaxSms) && sms <= kMaxSms
+               ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kErrorBytes)
+               : nullptr;
   a.ws = static_cast<uint32_t*>(workspace);
   a.num_sms = sms;
   return run_gemm(a, x, w, out, z, static_cast<cudaStream_t>(stream));

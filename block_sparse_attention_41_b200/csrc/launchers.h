@@ -206,9 +206,9 @@ struct GemmArgs {
   const float* bias;    // [No] or null
   const void* residual; // bf16 [Mo, No] or null
   int act;
-  bool store_z;
   void* out;
-  float* part;          // linear_part_bytes for the pieces of the last tiles, or null; only without an epilogue
+  void* z;              // or null
+  float* part;          // linear_part_bytes for the pieces of the last tiles, or null: none are split
   uint32_t* ws;         // error words or null
   int num_sms;
 };

@@ -16,7 +16,8 @@
 // tile, of which each CTA loads its 128 rows of A and its half of B's rows, and one thread issues the
 // MMAs for both. That halves what shared memory takes in per product for B; a tile of 128 x 256 on one
 // SM is held back there (1.22 PFLOP/s at 33272 x 4096 x 16384). Few tiles go to single SMs, 128 x 128 or
-// 128 x 64 each, to fill more of them.
+// 128 x 64 each, to fill more of them; with a long reduction and a workspace, the tiles past the last whole turn
+// of the SMs go in pieces of the reduction, which a second kernel adds (200 x 4096 -> 4096: 25 us whole, 16 us).
 //
 // With up to kFewRows rows the layer is bound by reading w once. There the product is taken
 // transposed: 128 rows of w are the M side of the MMA and the tokens its N side, so the ring holds
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         ++asked;
       };
-      const bool with_res = p.has_residual;  // past the last row too: zeros, so that every chunk counts alike
+      const bool with_res = p.has_residual && t < p.whole;  // past the last row too: zeros, so that every chunk counts alike
       if (with_res && tn * TN + c_lo < p.No) ask(tn * TN + c_lo, 1);
       float4 bias[8];  // of a chunk, read ahead as well
       auto read_bias = [&](int c) {
@@ -580,10 +581,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (warp == 1) pair_tmem_dealloc<CG>(tmem, C::TMEM_COLS);
 }
 
-// The pieces of the last tiles added, in order, and rounded: one warp per 32 x 32 outputs. Only products
-// without an epilogue (the gradients) are split.
+// The pieces of the last tiles added, in order, with the epilogue of the others: one warp per 32 x 32
+// outputs, a row of 32 to each lane.
+struct PieceArgs {
+  __nv_bfloat16* out;
+  __nv_bfloat16* z;               // or null
+  const __nv_bfloat16* residual;  // or null
+};
 template <int CG, int TN>
-__global__ void __launch_bounds__(256) sol_linear_pieces_kernel(const __grid_constant__ GemmParams p, __nv_bfloat16* out) {
+__global__ void __launch_bounds__(256) sol_linear_pieces_kernel(const __grid_constant__ GemmParams p, const PieceArgs a) {
   chained_wait();
   const int lane = threadIdx.x & 31, i = blockIdx.x * 8 + (threadIdx.x >> 5);
   constexpr int kChunks = CG * 4 * (TN / 32);
@@ -607,12 +613,47 @@ __global__ void __launch_bounds__(256) sol_linear_pieces_kernel(const __grid_con
     }
   }
   if (row >= p.Mo) return;
-  __nv_bfloat16* o = out + static_cast<size_t>(row) * p.No + col0;
+  const size_t o = static_cast<size_t>(row) * p.No + col0;
+  f2 v[16];
 #pragma unroll
-  for (int j = 0; j < 8; j += 2)
-    if (col0 + 4 * j < p.No)
-      *reinterpret_cast<uint4*>(o + 4 * j) = make_uint4(pack_bf16x2(s[j].x, s[j].y), pack_bf16x2(s[j].z, s[j].w),
-                                                        pack_bf16x2(s[j + 1].x, s[j + 1].y), pack_bf16x2(s[j + 1].z, s[j + 1].w));
+  for (int j = 0; j < 8; ++j) {
+    v[2 * j] = pack2(s[j].x, s[j].y);
+    v[2 * j + 1] = pack2(s[j].z, s[j].w);
+    if (p.bias != nullptr && col0 + 4 * j < p.No) {  // No is a multiple of 8
+      const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col0 + 4 * j));
+      v[2 * j] = add2(v[2 * j], pack2(b.x, b.y));
+      v[2 * j + 1] = add2(v[2 * j + 1], pack2(b.z, b.w));
+    }
+  }
+  auto put = [&](__nv_bfloat16* to) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2(v[4 * j + k]);
+        w[k] = pack_bf16x2(f.x, f.y);
+      }
+      if (col0 + 8 * j < p.No) *reinterpret_cast<uint4*>(to + o + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  };
+  if (a.z != nullptr) put(a.z);
+  with_activation(p.act, [&](auto kind) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = activate<decltype(kind)::value>(v[j]);
+  });
+  if (a.residual != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (col0 + 8 * j >= p.No) break;
+      const uint4 r = *reinterpret_cast<const uint4*>(a.residual + o + 8 * j);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[4 * j + k] = add2(v[4 * j + k], pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)));
+    }
+  }
+  put(a.out);
 }
 
 // ---- few rows --------------------------------------------------------------------------------------
@@ -911,8 +952,9 @@ cudaError_t launch_gemm_t(const GemmArgs& a, GemmParams p, cudaStream_t stream) 
                                         dim3(kGemmThreads), C::SMEM, stream, CG, a.maps[0], a.maps[1], a.maps[2], a.maps[3],
                                         a.maps[4], p);
   if (le != cudaSuccess || p.split == 1) return le;
-  return launch_chained(sol_linear_pieces_kernel<CG, TN>, dim3(rest * CG * 4 * (TN / 32) / 8), dim3(256), 0, stream, 1, p,
-                        static_cast<__nv_bfloat16*>(a.out));
+  const PieceArgs pieces = {static_cast<__nv_bfloat16*>(a.out), static_cast<__nv_bfloat16*>(a.z),
+                            static_cast<const __nv_bfloat16*>(a.residual)};
+  return launch_chained(sol_linear_pieces_kernel<CG, TN>, dim3(rest * CG * 4 * (TN / 32) / 8), dim3(256), 0, stream, 1, p, pieces);
 }
 
 template <bool A_MN, bool B_MN>
@@ -949,7 +991,8 @@ GemmTile linear_tile(int Mo, int No, int Ko, bool splittable, int num_sms) {
     const int rest = static_cast<int>(tiles % units);
     for (int split = 1; split == 1 || (splittable && rest > 0 && rest * split <= units && nk / split >= kPieceSlices); ++split) {
       const double turns = static_cast<double>(tiles / units) * nk + (rest > 0 ? std::ceil(nk / static_cast<double>(split)) : 0.0);
-      const double t = turns * o.slice + o.last + (split > 1 ? kPieceCycles : 0.0);
+      double t = turns * o.slice + o.last;
+      if (split > 1) t = 1.03 * (t + kPieceCycles);  // not for a few percent
       if (least == 0.0 || t < least) {
         least = t;
         best = {o.ctas, o.n, split};
@@ -979,7 +1022,7 @@ cudaError_t launch_linear_gemm(const GemmArgs& a, cudaStream_t stream) {
   p.bias = a.bias;
   p.has_residual = a.residual != nullptr;
   p.act = a.act;
-  p.store_z = a.store_z;
+  p.store_z = a.z != nullptr;
   p.part = a.part;
   p.ws = a.ws;
   if (a.a_mn) return launch_gemm_n<true, true>(a, p, stream);

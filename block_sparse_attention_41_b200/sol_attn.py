@@ -48,6 +48,7 @@ EXPORTED = (
     "sol_attn_rope_tables",
     "sol_attn_rope",
     "sol_attn_linear",
+    "sol_attn_linear_workspace_bytes",
     "sol_attn_linear_bwd",
     "sol_attn_linear_bwd_workspace_bytes",
 )
@@ -142,6 +143,8 @@ def load_library() -> ctypes.CDLL:
     lib.sol_attn_rope.restype = i32
     lib.sol_attn_linear.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, size, vp]
     lib.sol_attn_linear.restype = i32
+    lib.sol_attn_linear_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.sol_attn_linear_workspace_bytes.restype = size
     lib.sol_attn_linear_bwd_workspace_bytes.argtypes = [i32, i32, i32]
     lib.sol_attn_linear_bwd_workspace_bytes.restype = size
     lib.sol_attn_linear_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, size, vp]
@@ -885,8 +888,9 @@ def sol_attn_linear(x, w, bias=None, act: str = "none", residual=None, out=None,
                     workspace=None, stream=None):
     """residual + act(x w^T + bias): x bf16 [..., K], w bf16 [N, K], bias fp32 [N], residual bf16 [..., N];
     act "none", "gelu", "gelu_tanh" or "silu". Returns out, or (out, z) with z = x w^T + bias (bf16, for
-    sol_attn_linear_bwd) when want_z or a z tensor is given. workspace: a zeroed uint8 tensor of 256
-    bytes or more for sol_attn_check_device_error."""
+    sol_attn_linear_bwd) when want_z or a z tensor is given. workspace: a uint8 tensor whose first 256 bytes
+    are zeroed, for sol_attn_check_device_error; with sol_attn_linear_workspace_bytes bytes (the default)
+    a product of few tiles is split along K."""
     _check_linear("x", x, w)
     code = _choice("act", act, ACTIVATIONS)
     N, K = w.shape
@@ -906,11 +910,16 @@ def sol_attn_linear(x, w, bias=None, act: str = "none", residual=None, out=None,
     if _elsewhere(x, stream):
         with _On(x.device, stream):
             return sol_attn_linear(x, w, bias, act, residual, out, z, want_z, workspace)
+    lib = load_library()
     if out is None:
         out = x.new_empty(shape)
     if z is None and want_z:
         z = x.new_empty(shape)
-    st = load_library().sol_attn_linear(
+    if workspace is None and M > 128:
+        n = lib.sol_attn_linear_workspace_bytes(M, N, K)
+        if n > 256:  # the product wants to be split
+            workspace = x.new_empty(n, dtype=torch.uint8)
+    st = lib.sol_attn_linear(
         x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
         None if residual is None else residual.data_ptr(), code, M, N, K, out.data_ptr(), None if z is None else z.data_ptr(),
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), _raw_stream(index))

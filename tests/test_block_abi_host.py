@@ -160,6 +160,13 @@ def test_linear_workspace_bytes(lib):
     assert f(1 << 24, 64, 0) == f(1 << 22, 64, 0) <= 32 << 20
 
 
+def test_linear_forward_workspace_bytes(lib):
+    f = lib.sol_attn_linear_workspace_bytes
+    assert f(0, 8, 8) == f(8, 4, 8) == f(8, 8, 12) == f(1 << 28, 1 << 28, 8) == 0
+    assert f(128, 4096, 4096) == f(33272, 16384, 4096) == f(8191, 768, 768) == f(200, 768, 64) == 256
+    assert 256 < f(200, 4096, 4096) <= 32 << 20
+
+
 def test_linear_bindings_refuse_cpu_tensors(lib):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(TypeError):

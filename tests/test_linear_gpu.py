@@ -115,6 +115,29 @@ def test_many_large_tiles(M, N, K):
     same_bits(db, rb, "db")
 
 
+@pytest.mark.parametrize("M,N,K", [(129, 136, 4104), (200, 4096, 4096), (300, 72, 8192), (1000, 5120, 4104), (1500, 264, 4104)])
+def test_split_products_of_few_tiles(M, N, K):
+    lib = sa.load_library()
+    assert lib.sol_attn_linear_workspace_bytes(M, N, K) > 256
+    g = _gen(M, N, K, 7)
+    x, w, res = ints(g, -2, 2, M, K), ints(g, -2, 2, N, K), ints(g, -9, 9, M, N)
+    bias = torch.randint(-5, 6, (N,), generator=g, device="cuda").float()
+    ref, rz = bo.linear(_np(x), _np(w), _np(bias), "none", _np(res))
+    out, z = sa.sol_attn_linear(x, w, bias, residual=res, want_z=True)
+    same_bits(out, ref, "out")
+    same_bits(z, rz, "z")
+    again = res.clone()
+    assert torch.equal(sa.sol_attn_linear(x, w, bias, residual=again, out=again), out)  # in place of the residual
+    unsplit = sa.sol_attn_linear(x, w, bias, residual=res, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(unsplit, out)  # whole sums do not depend on the order
+    # an activation on split sums: the same z, so the same bits
+    for act in ("gelu", "gelu_tanh", "silu"):
+        small = (w.float() / 64).to(BF)
+        a = sa.sol_attn_linear(x, small, bias, act, res)
+        b = sa.sol_attn_linear(x, small, bias, act, res, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(a, b), act
+
+
 def sum_error(K):
     return 17 * (K / 16 + 1) * 2.0 ** -23
 
