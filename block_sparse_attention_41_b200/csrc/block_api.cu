@@ -315,8 +315,13 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
     return fail(SOL_EINVAL, "device pointers must be aligned to their elements");
   if (d > 512 || d % 2 != 0) return fail(SOL_EUNSUPPORTED, "rotary positions need an even d <= 512 (d=%d)", d);
   if (B > 65535 || static_cast<long long>(Hq) + Hk > 65535) return fail(SOL_EUNSUPPORTED, "B and Hq + Hk must be <= 65535");
-  const int V = dt == SOL_BF16 ? 8 : 4;
-  a.vec = layout == SOL_ROPE_HALF ? (rot / 2) % V == 0 && d % V == 0 : d % V == 0;
+  const int esize = dt == SOL_BF16 ? 2 : 4;
+  a.width = 16 / esize;
+  auto narrow_to = [&a](long long n) {
+    while (n % a.width != 0) a.width /= 2;
+  };
+  narrow_to(d);
+  narrow_to(layout == SOL_ROPE_HALF ? rot / 2 : rot);
   a.copy_rest = false;
   for (int i = 0; i < 2; ++i) {
     sol::RopeSide& r = a.side[i];
@@ -337,11 +342,13 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
       *dst[0][k] = in[k];
       *dst[1][k] = out[k];
       if (in[k] != out[k]) same = false;
-      if (in[k] % V != 0 || out[k] % V != 0) a.vec = false;
+      narrow_to(in[k]);
+      narrow_to(out[k]);
     }
     if (r.in == r.out && !same) return fail(SOL_EINVAL, "in place, input and output must have the same strides");
     if (!same) a.copy_rest = true;
-    if (!aligned16(r.in) || !aligned16(r.out)) a.vec = false;
+    narrow_to(static_cast<long long>(reinterpret_cast<uintptr_t>(r.in) % 16) / esize);
+    narrow_to(static_cast<long long>(reinterpret_cast<uintptr_t>(r.out) % 16) / esize);
   }
   int sms = 0;
   if ((st = current_device(&sms)) != SOL_OK) return st;

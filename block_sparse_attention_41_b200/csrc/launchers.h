@@ -171,7 +171,7 @@ struct RopeArgs {
   int end[4];            // pairs [end[a - 1], end[a]) turn by axis a
   float factor;
   bool half, inverse, bf16;
-  bool vec;              // 16-byte accesses
+  int width;             // values per access: it divides every length, stride and address
   bool copy_rest;        // channels [rot, d) have to be written too
 };
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);

@@ -11,8 +11,8 @@
 // 2^-32 of a turn. Cosine and sine of what is left of it in the nearest quarter turn come from their
 // Taylor series, good to about 1e-7 at every position. The 64-bit float work is one product per pair.
 //
-// HBM-bound: every element is read and written once. A thread owns one 16-byte vector of columns (a
-// vector of each half in the half layout) of one token, forms its cosines and sines once and then
+// HBM-bound: every element is read and written once. A thread owns one vector of columns, of 16 bytes where
+// lengths, strides and addresses allow (one of each half in the half layout), of one token, forms its cosines and sines once and then
 // runs over heads with them, so their cost is shared by all heads of a token. Input and output have
 // strides of their own: the same pass takes a token-major projection to head-major rows, or back.
 #include <cmath>
@@ -99,52 +99,72 @@ __device__ __forceinline__ void turns_of(const RopeArgs& p, int b, int t, int i,
   }
 }
 
+// V values as 32-bit words, in one access of 4, 8 or 16 bytes (WIDE) or one by one.
 template <typename T, int V>
+using Words = uint32_t[V * sizeof(T) / 4 > 0 ? V * sizeof(T) / 4 : 1];
+template <typename T, int V>
+__device__ __forceinline__ void load_wide(const T* p, Words<T, V>& w) {
+  if constexpr (V * sizeof(T) == 16) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (V * sizeof(T) == 8) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_wide(T* p, const Words<T, V>& w) {
+  if constexpr (V * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else if constexpr (V * sizeof(T) == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(p) = w[0];
+}
+
+// V values, as fp32 and as they were read: a store may keep those (infinities and NaN included).
+template <typename T, int V, bool WIDE>
 struct Vec {
+  enum : int { kWords = V * static_cast<int>(sizeof(T)) / 4 };
   float x[V];
+  Words<T, V> w;
+  T one[WIDE ? 1 : V];
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (V == 8) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (WIDE) {
+      load_wide<T, V>(p, w);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      for (int k = 0; k < V; ++k) {
+        if constexpr (sizeof(T) == 4) x[k] = __uint_as_float(w[k]);
+        else x[k] = __uint_as_float(k % 2 == 0 ? w[k / 2] << 16 : w[k / 2] & 0xffff0000u);
       }
-    } else if constexpr (V == 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
     } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[k] = static_cast<float>(p[k]);
+      for (int k = 0; k < V; ++k) {
+        one[k] = p[k];
+        x[k] = static_cast<float>(one[k]);
+      }
     }
   }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (V == 8) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    } else if constexpr (V == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    } else if constexpr (sizeof(T) == 2) {
+  __device__ __forceinline__ void store(T* p, bool as_read) const {
+    if constexpr (WIDE) {
+      Words<T, V> o;
 #pragma unroll
-      for (int k = 0; k < V; ++k) p[k] = __float2bfloat16_rn(x[k]);
+      for (int k = 0; k < kWords; ++k) {
+        if constexpr (sizeof(T) == 4) o[k] = __float_as_uint(x[k]);
+        else o[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+        if (as_read) o[k] = w[k];
+      }
+      store_wide<T, V>(p, o);
     } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) p[k] = x[k];
+      for (int k = 0; k < V; ++k) {
+        T o;
+        if constexpr (sizeof(T) == 2) o = __float2bfloat16_rn(x[k]);
+        else o = x[k];
+        p[k] = as_read ? one[k] : o;
+      }
     }
   }
 };
-
-// V values moved as bits.
-template <typename T, int V>
-__device__ __forceinline__ void copy_vec(T* out, const T* in) {
-  if constexpr (V * sizeof(T) == 16) {
-    *reinterpret_cast<uint4*>(out) = __ldg(reinterpret_cast<const uint4*>(in));
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; ++k) out[k] = in[k];
-  }
-}
 
 // Calls f(in, out) for heads [h0, h1) of the queries followed by the keys.
 template <typename T, typename F>
@@ -160,27 +180,14 @@ __device__ __forceinline__ void for_heads(const RopeArgs& p, int b, int t, int h
   }
 }
 
-// The first heads' vectors on their way to L2 while the cosines and sines are formed: a block has nothing
-// else in flight then. (75600 tokens of 80 heads of 128, bf16: 568 us without, 556 with 8 heads, 553 with
-// 12 or 16, 568 with 24.)
-constexpr int kAhead = 12;
-template <typename T>
-__device__ __forceinline__ void ask_ahead(const RopeArgs& p, int b, int t, int h0, int h1, int col) {
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int h = h0 + k;
-    if (h >= h1) break;
-    const int s = h >= p.side[0].heads;
-    const RopeSide& r = p.side[s];
-    const T* in = static_cast<const T*>(r.in) + b * r.in_b + t * r.in_l + (h - (s ? p.side[0].heads : 0)) * r.in_h + col;
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(in));
-  }
-}
+// A pass with channels that only pass through has them in the same loop as the turned ones, where the
+// store chooses: threads of a warp that took loops of their own would wait for one another. Without such
+// channels the loop has no choice in it (75600 tokens of 80 heads of 128, bf16: 488 us, 567 with one: it
+// kept the loads of several heads from going out together).
 
-// Interleaved pairs: N columns of consecutive pairs per thread. V = N: one vector. V = 2 values is
-// one pair read and written as scalars.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) sol_rope_interleaved_kernel(const __grid_constant__ RopeArgs p, int groups,
+// Interleaved pairs: V columns of consecutive pairs per thread.
+template <typename T, int V, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 8) sol_rope_interleaved_kernel(const __grid_constant__ RopeArgs p, int groups,
                                                                          int heads_per_block) {
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int t = static_cast<int>(i / groups), g = static_cast<int>(i - static_cast<long long>(t) * groups);
@@ -189,44 +196,31 @@ __global__ void __launch_bounds__(kThreads) sol_rope_interleaved_kernel(const __
   const int b = blockIdx.z, col = g * V;
   const int heads = p.side[0].heads + p.side[1].heads;
   const int h0 = blockIdx.y * heads_per_block, h1 = min(h0 + heads_per_block, heads);
-  if (col >= p.rot) {  // the rest passes through as bits, infinities and NaN included
+  const bool keep = col >= p.rot;
+  float c[V / 2], s[V / 2];
+  turns_of<V / 2>(p, b, t, col / 2, p.rot / 2, c, s);
+  auto run = [&](bool as_read) {
     for_heads<T>(p, b, t, h0, h1, [&](const T* in, T* out, long long ih, long long oh, int lo, int hi) {
 #pragma unroll 4
-      for (int h = lo; h < hi; ++h) copy_vec<T, V>(out + h * oh + col, in + h * ih + col);
-    });
-    return;
-  }
-  const int turned = min(V, p.rot - col);  // a vector across the border: its first values turn
-  float c[V / 2], s[V / 2];
-  ask_ahead<T>(p, b, t, h0, h1, col);
-  turns_of<V / 2>(p, b, t, col / 2, p.rot / 2, c, s);
-  for_heads<T>(p, b, t, h0, h1, [&](const T* in, T* out, long long ih, long long oh, int lo, int hi) {
-#pragma unroll 4
-    for (int h = lo; h < hi; ++h) {
-      Vec<T, V> v;
-      v.load(in + h * ih + col);
+      for (int h = lo; h < hi; ++h) {
+        Vec<T, V, WIDE> v;
+        v.load(in + h * ih + col);
 #pragma unroll
-      for (int k = 0; k < V / 2; ++k) {
-        const float a = v.x[2 * k], q = v.x[2 * k + 1];
-        v.x[2 * k] = fmaf(a, c[k], -q * s[k]);
-        v.x[2 * k + 1] = fmaf(a, s[k], q * c[k]);
-      }
-      if (turned == V) {
-        v.store(out + h * oh + col);
-      } else {
-        for (int k = 0; k < V; ++k) {
-          T* o = out + h * oh + col + k;
-          if (k >= turned) *o = in[h * ih + col + k];
-          else if constexpr (sizeof(T) == 2) *o = __float2bfloat16_rn(v.x[k]);
-          else *o = v.x[k];
+        for (int k = 0; k < V / 2; ++k) {
+          const float a = v.x[2 * k], q = v.x[2 * k + 1];
+          v.x[2 * k] = fmaf(a, c[k], -q * s[k]);
+          v.x[2 * k + 1] = fmaf(a, s[k], q * c[k]);
         }
+        v.store(out + h * oh + col, as_read);
       }
-    }
-  });
+    });
+  };
+  if (groups * V == p.rot) run(false);
+  else run(keep);
 }
 
-// Half layout: V pairs per thread, (i, i + rot / 2); groups past those copy V channels of the rest.
-template <typename T, int V>
+// Half layout: V pairs per thread, (i, i + rot / 2); groups past those pass two vectors of the rest through.
+template <typename T, int V, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 8) sol_rope_half_kernel(const __grid_constant__ RopeArgs p, int groups,
                                                                   int heads_per_block) {
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
@@ -236,43 +230,41 @@ __global__ void __launch_bounds__(kThreads, 8) sol_rope_half_kernel(const __grid
   const int b = blockIdx.z, half = p.rot / 2;
   const int heads = p.side[0].heads + p.side[1].heads;
   const int h0 = blockIdx.y * heads_per_block, h1 = min(h0 + heads_per_block, heads);
-  if (g * V >= half) {
-    const int col = p.rot + g * V - half;
+  const bool keep = g * V >= half;
+  const int first = keep ? p.rot + 2 * (g * V - half) : g * V;
+  const bool both = !keep || first + V < p.d;
+  const int second = !keep ? first + half : both ? first + V : first;
+  float c[V], s[V];
+  turns_of<V>(p, b, t, g * V, half, c, s);
+  auto run = [&](bool as_read, bool two) {
     for_heads<T>(p, b, t, h0, h1, [&](const T* in, T* out, long long ih, long long oh, int lo, int hi) {
 #pragma unroll 4
-      for (int h = lo; h < hi; ++h) copy_vec<T, V>(out + h * oh + col, in + h * ih + col);
-    });
-    return;
-  }
-  const int col = g * V;
-  float c[V], s[V];
-  ask_ahead<T>(p, b, t, h0, h1, col);
-  ask_ahead<T>(p, b, t, h0, h1, col + half);
-  turns_of<V>(p, b, t, col, half, c, s);
-  for_heads<T>(p, b, t, h0, h1, [&](const T* in, T* out, long long ih, long long oh, int lo, int hi) {
-#pragma unroll 4
-    for (int h = lo; h < hi; ++h) {
-      Vec<T, V> u, w;
-      u.load(in + h * ih + col);
-      w.load(in + h * ih + col + half);
+      for (int h = lo; h < hi; ++h) {
+        Vec<T, V, WIDE> u, w;
+        u.load(in + h * ih + first);
+        w.load(in + h * ih + second);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float a = u.x[k], q = w.x[k];
-        u.x[k] = fmaf(a, c[k], -q * s[k]);
-        w.x[k] = fmaf(a, s[k], q * c[k]);
+        for (int k = 0; k < V; ++k) {
+          const float a = u.x[k], q = w.x[k];
+          u.x[k] = fmaf(a, c[k], -q * s[k]);
+          w.x[k] = fmaf(a, s[k], q * c[k]);
+        }
+        u.store(out + h * oh + first, as_read);
+        if (two) w.store(out + h * oh + second, as_read);
       }
-      u.store(out + h * oh + col);
-      w.store(out + h * oh + col + half);
-    }
-  });
+    });
+  };
+  if (groups * V == half) run(false, true);
+  else run(keep, both);
 }
 
 template <typename T, int V>
 cudaError_t launch_t(const RopeArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr bool WIDE = V * sizeof(T) >= 4 && V > 1;
   constexpr int VI = V == 1 ? 2 : V;  // an interleaved group is at least one pair
-  // V divides every width here (the caller's rule for vec); a scalar group is one pair or channel
+  // V divides every width here (the caller's rule); a group of single values is one pair or channel
   const int rest = a.copy_rest ? a.d - a.rot : 0;
-  const int groups = a.half ? a.rot / 2 / V + rest / V : (a.rot + rest + VI - 1) / VI;
+  const int groups = a.half ? a.rot / 2 / V + (rest / V + 1) / 2 : (a.rot + rest) / VI;
   const long long blocks = (static_cast<long long>(a.L) * groups + kThreads - 1) / kThreads;
   const int heads = a.side[0].heads + a.side[1].heads;
   // Heads of one token share their cosines: as many per block as leave eight blocks per SM, but at
@@ -282,7 +274,7 @@ cudaError_t launch_t(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   int hpb = static_cast<int>((heads + split - 1) / split);
   if (hpb < 4) hpb = heads < 4 ? heads : 4;
   const dim3 grid(static_cast<unsigned>(blocks), (heads + hpb - 1) / hpb, a.B);
-  return launch_chained(a.half ? sol_rope_half_kernel<T, V> : sol_rope_interleaved_kernel<T, VI>, grid, dim3(kThreads), 0, stream, 1,
+  return launch_chained(a.half ? sol_rope_half_kernel<T, V, WIDE> : sol_rope_interleaved_kernel<T, VI, WIDE>, grid, dim3(kThreads), 0, stream, 1,
                         a, groups, hpb);
 }
 
@@ -347,8 +339,21 @@ __global__ void __launch_bounds__(kTableThreads) sol_rope_tables_kernel(const __
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.bf16) return a.vec ? launch_t<__nv_bfloat16, 8>(a, num_sms, stream) : launch_t<__nv_bfloat16, 1>(a, num_sms, stream);
-  return a.vec ? launch_t<float, 4>(a, num_sms, stream) : launch_t<float, 1>(a, num_sms, stream);
+  // the widest access that divides every length, stride and address (half layout, 40000 tokens of 32 heads of
+  // 128: 281 us with 94 channels turned, pair by pair, 133 with 92, two pairs at a time, 114 with 88, four)
+  if (a.bf16) {
+    switch (a.width) {
+      case 8: return launch_t<__nv_bfloat16, 8>(a, num_sms, stream);
+      case 4: return launch_t<__nv_bfloat16, 4>(a, num_sms, stream);
+      case 2: return launch_t<__nv_bfloat16, 2>(a, num_sms, stream);
+      default: return launch_t<__nv_bfloat16, 1>(a, num_sms, stream);
+    }
+  }
+  switch (a.width) {
+    case 4: return launch_t<float, 4>(a, num_sms, stream);
+    case 2: return launch_t<float, 2>(a, num_sms, stream);
+    default: return launch_t<float, 1>(a, num_sms, stream);
+  }
 }
 
 cudaError_t launch_rope_tables(const RopeTableArgs& a, int num_sms, cudaStream_t stream) {

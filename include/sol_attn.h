@@ -431,8 +431,8 @@ sol_status sol_attn_rope_tables(const int32_t* pos, int axes, const int* section
  *                out, or back for a gradient, need no copy of their own
  *   pos          device, int32 [axes, L] per batch entry, pos_stride_b elements apart (0: shared)
  *   sections, inv_freq, attn_factor as above
- * Even d <= 512, any even rot <= d. 16-byte accesses where addresses, strides, d and (half layout)
- * rot / 2 allow them, single ones elsewhere. B <= 65535, Hq + Hk <= 65535. */
+ * Even d <= 512, any even rot <= d. Accesses of 16 bytes where addresses, strides, d and (half layout)
+ * rot / 2 allow them, else of 8, 4 or single values. B <= 65535, Hq + Hk <= 65535. */
 sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides,
                          sol_dtype dt, const int32_t* pos, int64_t pos_stride_b, int axes,
                          const int* sections, const double* inv_freq, float attn_factor,

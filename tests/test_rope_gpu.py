@@ -91,6 +91,29 @@ def test_far_positions_and_position_axes(layout, start):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("d,rot", [(128, 96), (128, 88), (128, 92), (128, 94), (72, 72), (68, 40), (66, 12), (20, 8)])
+@pytest.mark.parametrize("shift", [0, 1, 2, 4, 8])
+def test_every_width_of_access(layout, dtype, d, rot, shift):
+    """Lengths, strides and addresses that divide by 8, 4, 2 or 1 values."""
+    B, H, L = 2, 3, 21
+    g = torch.Generator(device="cuda").manual_seed(d + rot + shift)
+    wide = torch.randn((B, L, H, d + shift + (-d - shift) % 8), generator=g, device="cuda").to(DT[dtype])
+    q = wide[..., shift:shift + d].transpose(1, 2)
+    f, _ = sa.sol_attn_rope_inv_freq(rot, device="cuda")
+    pos = torch.arange(L, dtype=torch.int32, device="cuda") * 11
+    ref, _ = sa.sol_attn_rope(q.contiguous(), None, pos, f, layout=layout)
+    check(ref, q, pos, f, None, 1.0, layout, False, dtype)
+    got, _ = sa.sol_attn_rope(q, None, pos, f, layout=layout)
+    assert torch.equal(got, ref)
+    back = torch.full_like(wide, 7.0)  # the gradient into a slice, the rest stays
+    sa.sol_attn_rope(ref, None, pos, f, layout=layout, inverse=True, Q_out=back[..., shift:shift + d].transpose(1, 2))
+    want, _ = sa.sol_attn_rope(ref, None, pos, f, layout=layout, inverse=True)
+    assert torch.equal(back[..., shift:shift + d].transpose(1, 2), want)
+    assert bool((back[..., :shift] == 7.0).all()) and bool((back[..., shift + d:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
 @pytest.mark.parametrize("d,pad", [(64, 0), (64, 8), (48, 3)])
 def test_token_major_in_and_out(layout, dtype, d, pad):
     B, Hq, Hk, L = 2, 6, 3, 37
