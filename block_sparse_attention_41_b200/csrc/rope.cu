@@ -11,10 +11,11 @@
 // 2^-32 of a turn. Cosine and sine of what is left of it in the nearest quarter turn come from their
 // Taylor series, good to about 1e-7 at every position. The 64-bit float work is one product per pair.
 //
-// HBM-bound: every element is read and written once. A thread owns one vector of columns, of 16 bytes where
-// lengths, strides and addresses allow (one of each half in the half layout), of one token, forms its cosines and sines once and then
-// runs over heads with them, so their cost is shared by all heads of a token. Input and output have
-// strides of their own: the same pass takes a token-major projection to head-major rows, or back.
+// HBM-bound: every element is read and written once. A thread owns one vector of columns of one token
+// (one of each half in the half layout), of 16 bytes where lengths, strides and addresses allow. It forms
+// its cosines and sines once and then runs over heads with them, so their cost is shared by all heads of
+// a token. Input and output have strides of their own: the same pass takes a token-major projection to
+// head-major rows, or back. 75600 tokens of 80 heads of 128 bf16: 488 us, 6.3 TB/s.
 #include <cmath>
 
 #include "chained.cuh"
