@@ -571,7 +571,7 @@ def tau_list(values) -> list:
 # that find out what is wrong with it. Together they took a call on four tokens from 22 to 15 us.
 _I64x3 = ctypes.c_int64 * 3
 _F32, _BF16 = torch.float32, torch.bfloat16
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # torch built without CUDA has no tensors for these calls
 
 
 def _fits(t, index: int, dtype, shape) -> bool:
