@@ -6,6 +6,8 @@
 // turn then hold each other's places: 45 us for the same norm gradient.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 namespace sol {
@@ -30,6 +32,20 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t s
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// A kernel's dynamic shared memory is allowed once per device, at the largest size that any of its launches
+// takes: the attribute is the kernel's, so a launch that set its own size would take it from another thread's.
+template <auto Kernel>
+cudaError_t allow_smem(int most) {
+  constexpr int kDevices = 64;
+  static std::atomic<bool> done[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < kDevices && done[dev].load(std::memory_order_relaxed))) return e;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess && dev < kDevices) done[dev].store(true, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace sol

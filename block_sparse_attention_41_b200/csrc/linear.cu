@@ -28,7 +28,6 @@
 //
 // Every wait is bounded: on expiry the CTA records the timeout in the caller's workspace (where one
 // is given), lets its copies and MMAs in flight end, frees its tensor memory and returns.
-#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -918,19 +917,6 @@ __global__ void __launch_bounds__(512) sol_linear_db_kernel(const float* __restr
     for (int i = 0; i < 16; ++i) t += s[i][threadIdx.x];
     db[col] = t;
   }
-}
-
-// A kernel's dynamic shared memory is allowed once per device.
-template <auto Kernel>
-cudaError_t allow_smem(int bytes) {
-  constexpr int kDevices = 64;
-  static std::atomic<bool> done[kDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < kDevices && done[dev].load(std::memory_order_relaxed))) return e;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < kDevices) done[dev].store(true, std::memory_order_relaxed);
-  return e;
 }
 
 template <int CG, int TN, bool A_MN, bool B_MN>

@@ -29,7 +29,7 @@ namespace {
 constexpr int kMaxWarps = 32;  // of a row
 constexpr int kSlot = 512;     // 16 bytes of each of a warp's threads
 constexpr int kMaxRows = 16;   // of several warps in a block: 15 named barriers
-constexpr int kSmemMax = 227 * 1024;  // per block
+constexpr int kSmemMax = 227 * 1024 - 10240;  // of a block's dynamic shared memory, beside the exchange buffers
 
 // ---- element access ------------------------------------------------------------------------------------
 // A 16-byte vector (V = 8 bf16 or 4 fp32) as V / 2 pairs, and back.
@@ -709,7 +709,7 @@ cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t s
   if (rows > share) rows = share;
   rows = (rows + unit - 1) / unit * unit;
   if constexpr (RING) {
-    const long long fit = static_cast<long long>((kSmemMax - 10240 - products) / row) / unit * unit;
+    const long long fit = static_cast<long long>((kSmemMax - products) / row) / unit * unit;
     if (rows > fit) rows = fit;
   }
   s.rpb = static_cast<int>(rows);
@@ -719,11 +719,8 @@ cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t s
   long long chunks = per_sm * num_sms / a.B, most = (a.T + s.rpb - 1) / s.rpb;
   if (chunks > most) chunks = most;
   if (chunks < 1) chunks = 1;
-  if (smem > 36 * 1024) {  // beyond 48 KB with the static part
-    const cudaError_t e = cudaFuncSetAttribute(sol_residual_norm_kernel<T, V, E, RING, FULL, MAXT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem<sol_residual_norm_kernel<T, V, E, RING, FULL, MAXT>>(kSmemMax);
+  if (e != cudaSuccess) return e;
   return launch_chained(sol_residual_norm_kernel<T, V, E, RING, FULL, MAXT>, dim3(static_cast<unsigned>(a.B * chunks)),
                         dim3(s.threads), smem, stream, 1, a, s.tpr, static_cast<int>(chunks));
 }
@@ -731,7 +728,7 @@ template <typename T, int V, bool FULL>
 cudaError_t launch_fwd(const NormArgs& a, const Shape& s, int num_sms, cudaStream_t stream) {
   if constexpr (V > 1) {
     // two rows in the ring; fp32 rows of more than 7680 channels leave it no room and are read directly
-    if (static_cast<size_t>(s.tpr) * s.elems * (12 + 4 * sizeof(T)) <= kSmemMax - 10240)
+    if (static_cast<size_t>(s.tpr) * s.elems * (12 + 4 * sizeof(T)) <= kSmemMax)
       return s.elems == 8 ? launch_fwd_k<T, V, 8, true, FULL, 1024>(a, s, num_sms, stream)
                           : launch_fwd_k<T, V, 16, true, FULL, 1024>(a, s, num_sms, stream);
   }
@@ -743,11 +740,8 @@ template <typename T, int V, int E, bool RING, bool FULL, int MAXT, int MINB>
 cudaError_t launch_bwd_k(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
   size_t smem = row_bytes(s, 8 + (RING ? 8 : 0) * static_cast<int>(sizeof(T)));
   if (s.rpb > 1 && smem < 12u * a.C) smem = 12u * a.C;  // the sums of a block's rows take the slots' place
-  if (smem > 36 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(sol_residual_norm_bwd_kernel<T, V, E, RING, FULL, MAXT, MINB>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem<sol_residual_norm_bwd_kernel<T, V, E, RING, FULL, MAXT, MINB>>(kSmemMax);
+  if (e != cudaSuccess) return e;
   return launch_chained(sol_residual_norm_bwd_kernel<T, V, E, RING, FULL, MAXT, MINB>, dim3(a.fwd.B * a.chunks), dim3(s.threads),
                         smem, stream, 1, a, s.tpr);
 }
@@ -764,7 +758,7 @@ template <typename T, int V, bool FULL>
 cudaError_t launch_bwd(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
   if constexpr (V > 1) {
     // two rows in the ring where they fit; fp32 rows of more than 5376 channels are read directly
-    if (row_bytes(s, 8 + 8 * static_cast<int>(sizeof(T))) <= kSmemMax - 10240)
+    if (row_bytes(s, 8 + 8 * static_cast<int>(sizeof(T))) <= kSmemMax)
       return s.elems == 8 ? launch_bwd_t<T, V, 8, true, FULL>(a, s, stream)
                           : launch_bwd_t<T, V, 16, true, FULL>(a, s, stream);
   }
