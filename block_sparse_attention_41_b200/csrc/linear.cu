@@ -65,7 +65,9 @@ struct GemmCfg {
   static constexpr int NS = 196608 / STAGE;  // 6 or 8 slices of 32 or 24 KB
   static constexpr int OFF_EPI = NS * STAGE;
   static constexpr int OFF_BAR = OFF_EPI + kEpiWarps * 2 * kEpiBuf;
+  static constexpr int OFF_COUNT = OFF_BAR + 16 * NS + 48 + 16 * kEpiWarps;  // behind the barriers
   static constexpr int SMEM = OFF_BAR + 384 + 1024;  // + alignment of the ring to 1024 bytes
+  static_assert(OFF_COUNT + 16 <= OFF_BAR + 384, "barriers and flags");
   static constexpr int TMEM_COLS = 2 * TN;
 };
 
@@ -252,6 +254,12 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Two counts to the other CTA of the pair: 8 bytes to `dst`, reported to `bar`, both as they lie in this CTA.
+__device__ __forceinline__ void send_counts(uint32_t dst, uint32_t bar, uint32_t to, uint32_t a, uint32_t b) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
+               ::"r"(in_cta(dst, to)), "l"(static_cast<uint64_t>(b) << 32 | a), "r"(in_cta(bar, to))
+               : "memory");
+}
 // All threads of the CTA, or of the pair.
 template <int CG>
 __device__ __forceinline__ void pair_sync() {
@@ -271,6 +279,17 @@ constexpr uint32_t instr_desc(int M, int N, bool a_mn, bool b_mn) {
 
 __device__ __forceinline__ int ring_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
   return mbar_wait(bar, parity, abort_flag, kWaitLimitNs);
+}
+
+// Before a CTA's shared memory is released: every commit to its barriers has arrived. Commits to different
+// barriers arrive in no stated order, so the last phase of each is waited for: `slices` commits went around
+// the ring, `accs` to the accumulators' barriers, one to `bar_last`.
+template <int NS>
+__device__ __forceinline__ void settle(uint32_t bar_empty, uint32_t slices, uint32_t bar_acc, uint32_t accs, uint32_t bar_last) {
+  for (uint32_t i = slices > NS ? slices - NS : 0; i < slices; ++i)
+    mbar_wait(bar_empty + 8 * (i % NS), (i / NS) & 1u, nullptr, kWaitLimitNs);
+  for (uint32_t i = accs > 2 ? accs - 2 : 0; i < accs; ++i) mbar_wait(bar_acc + 8 * (i & 1u), (i >> 1) & 1u, nullptr, kWaitLimitNs);
+  mbar_wait(bar_last, 0, nullptr, kWaitLimitNs);
 }
 
 // One 64-deep slice of an operand: `rows` rows along its M or N side, starting at r0, reduction from
@@ -332,9 +351,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* smem = smem_raw + (sb - raw);
   const uint32_t bars = sb + C::OFF_BAR;
   const uint32_t bar_full = bars, bar_empty = bars + 8 * C::NS, bar_acc = bars + 16 * C::NS,
-                 bar_free = bar_acc + 16, bar_drain = bar_free + 16, bar_res = bar_drain + 8;
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 16 * C::NS + 40 + 16 * kEpiWarps);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 16 * C::NS + 44 + 16 * kEpiWarps);
+                 bar_free = bar_acc + 16, bar_drain = bar_free + 16, bar_res = bar_drain + 8,
+                 bar_count = bar_res + 16 * kEpiWarps;
+  volatile uint32_t* s_count = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_COUNT);  // from the other CTA of a pair
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_COUNT + 8);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_COUNT + 12);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 1 ? 0u : cluster_rank();  // rank 0 issues the MMAs of a pair
@@ -348,6 +369,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(bar_free + 8 * a, CG * kEpiWarps);  // of a pair only rank 0's
     }
     mbar_init(bar_drain, 1);
+    mbar_init(bar_count, 1);
     for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(bar_res + 8 * i, 1);
     fence_mbar_init();
     *s_abort = 0;
@@ -385,26 +407,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_PRODUCER);
-      // No copy may be in flight when shared memory is released: the last use of every slice. Rank 1 cannot
-      // see its own land, but every MMA that reads them has ended when the last commit arrives here, and with
-      // it every other commit to this CTA's barriers; after an abort it waits a while for the rest.
+      // No copy and no commit may be on its way here when shared memory is released. Copies are seen on rank 0's
+      // full barriers only, commits in each CTA for itself, so of a pair rank 1 tells rank 0 how many slices it
+      // has loaded, and rank 0's MMA thread tells rank 1 how many commits it has issued.
+      bool told = false;
+      if constexpr (CG == 2) {
+        if (rank == 1) send_counts(sb + C::OFF_COUNT, bar_count, 0, g, 0);
+        mbar_arrive_expect_tx(bar_count, 8);
+        told = mbar_wait(bar_count, 0, nullptr, 2 * kWaitLimitNs) == WAIT_OK;
+      }
       if (rank == 0) {
-        for (uint32_t i = g > C::NS ? g - C::NS : 0; i < g; ++i)
+        uint32_t last = g;
+        // after an abort rank 1 may be ahead: slices that this CTA has not announced, with rank 1's bytes alone
+        for (; told && last < s_count[0]; ++last) mbar_arrive_expect_tx(bar_full + 8 * (last % C::NS), C::STAGE);
+        for (uint32_t i = last > C::NS ? last - C::NS : 0; i < last; ++i)
           mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, kWaitLimitNs);
       } else {
-        mbar_wait(bar_drain, 0, nullptr, 2 * kWaitLimitNs);
-        if (w != WAIT_OK) {
-          const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 1000000ull) {
-          }
-        }
+        settle<C::NS>(bar_empty, told ? s_count[0] : 0u, bar_acc, told ? s_count[1] : 0u, bar_drain);
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = instr_desc(CG * BM, TN, A_MN, B_MN);
       const uint64_t da0 = operand_desc<A_MN>(sb), db0 = operand_desc<B_MN>(sb + C::A_BYTES);
-      uint32_t g = 0, it = 0;
+      uint32_t g = 0, it = 0, done = 0;  // slices and tiles committed
       int w = WAIT_OK;
       for (int t = first; t < units && w == WAIT_OK; t += step, ++it) {
         const Unit un = unit_of(p, t);
@@ -426,11 +452,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                          (k > un.k_lo || kk > 0) ? 1u : 0u);
           pair_commit<CG>(bar_empty + 8 * s);
         }
-        if (w == WAIT_OK) pair_commit<CG>(bar_acc + 8 * acc);
+        if (w == WAIT_OK) {
+          pair_commit<CG>(bar_acc + 8 * acc);
+          ++done;
+        }
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_MMA);
       pair_commit<CG>(bar_drain);  // no MMA may be in flight when tensor memory is freed
-      mbar_wait(bar_drain, 0, nullptr, kWaitLimitNs);
+      if constexpr (CG == 2) send_counts(sb + C::OFF_COUNT, bar_count, 1, g, done);
+      settle<C::NS>(bar_empty, g, bar_acc, done, bar_drain);
     }
     __syncwarp();
   } else {
@@ -759,7 +789,7 @@ __global__ void __launch_bounds__(kFewThreads)
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_MMA);
       tc_commit(bar_acc);  // also after an abort: the MMAs in flight end before tensor memory is freed
-      mbar_wait(bar_acc, 0, nullptr, kWaitLimitNs);
+      settle<C::NS>(bar_empty, g, bar_acc, 0, bar_acc);
     }
     __syncwarp();
   } else {
