@@ -19,6 +19,10 @@ sol_status cuda_fail(cudaError_t e, const char* what);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool size_ok(long long v, long long lim) { return v >= 1 && v <= lim; }
 
+// The failure-detection test hook, taken by the launch that it is for (the attention or a linear layer): what the launch
+// leaves out, or 0, and the limit of its device waits.
+int take_drop(bool linear, uint64_t* wait_limit_ns);
+
 // An sm_100 GPU is current: SOL_OK and its SM count.
 sol_status current_device(int* num_sms);
 

@@ -127,6 +127,7 @@ sol_status run_gemm(sol::GemmArgs& a, const void* A, const void* Bm, void* out, 
   if (a.residual != nullptr &&
       (st = make_map2d(&a.maps[4], a.residual, a.No, a.Mo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != SOL_OK)
     return st;
+  a.drop = take_drop(true, &a.wait_limit_ns);
   const cudaError_t e = sol::launch_linear_gemm(a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "linear layer launch");
   return SOL_OK;
@@ -404,6 +405,7 @@ sol_status sol_attn_linear(const void* x, const void* w, const float* bias, cons
     a.act = act;
     a.ws = static_cast<uint32_t*>(workspace);
     a.num_sms = sms;
+    a.drop = take_drop(true, &a.wait_limit_ns);
     const cudaError_t e = sol::launch_linear_few(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "linear layer launch");
     return SOL_OK;

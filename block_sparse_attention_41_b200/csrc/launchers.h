@@ -187,6 +187,9 @@ struct RopeTableArgs {
 cudaError_t launch_rope_tables(const RopeTableArgs& a, int num_sms, cudaStream_t stream);
 
 // Linear layer (sol_attn_linear) and its gradients: bf16 operands, fp32 accumulation.
+// The copy that a launch leaves out (sol_attn_debug_drop_one_load): one of the attention, of the second operand's
+// in the launch's first or second CTA, or of the residual's.
+enum : int { DROP_ATTENTION = 1, DROP_OPERAND = 2, DROP_OPERAND_SECOND = 3, DROP_RESIDUAL = 4 };
 enum : int { ACT_NONE = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_SILU = 3 };
 constexpr int kFewRows = 128;  // up to here the forward takes the kernel for few rows
 constexpr int kDzBlocks = 1184;  // blocks of the dz pass: 8 per SM
@@ -209,6 +212,8 @@ struct GemmArgs {
   void* out;
   void* z;              // or null
   float* part;          // linear_part_bytes for the pieces of the last tiles, or null: none are split
+  int drop;             // failure-detection test hook, as the limit of a device wait
+  uint64_t wait_limit_ns;
   uint32_t* ws;         // error words or null
   int num_sms;
 };
@@ -221,6 +226,8 @@ struct FewArgs {
   void* out;
   void* z;  // or null
   int act;
+  int drop;
+  uint64_t wait_limit_ns;
   uint32_t* ws;
   int num_sms;
 };

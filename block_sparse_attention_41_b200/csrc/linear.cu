@@ -48,7 +48,6 @@ constexpr int kEpiBuf = 32 * 64;   // one warp's staging buffer: 32 rows x 32 bf
 // second kernel.
 constexpr int kPieceSlices = 16;
 constexpr double kPieceCycles = 9000.0;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // Output rows walked together, column by column: at least 2048, so that a wave of tiles is about square
 // and its tiles share operands as they stream by; with a short reduction as many as keep their part
 // of A in L2 while B passes (at K = 4096, 4096 rows instead of 2048: 2907 against 2968 us).
@@ -80,6 +79,8 @@ struct GemmParams {
   const float* bias;               // [No] or null
   int act;
   int has_residual, store_z;
+  int drop;      // DROP_*: a copy left out, for the tests of expired waits
+  uint64_t wait_limit_ns;
   uint32_t* ws;  // error words, or null
 };
 
@@ -277,19 +278,21 @@ constexpr uint32_t instr_desc(int M, int N, bool a_mn, bool b_mn) {
   return idesc_bf16_f32(M, N, b_mn) | (a_mn ? 1u << 15 : 0u);
 }
 
-__device__ __forceinline__ int ring_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-  return mbar_wait(bar, parity, abort_flag, kWaitLimitNs);
+// For the tests of expired waits: does this CTA leave out its copy of an operand's slice `g`?
+__device__ __forceinline__ bool left_out(int drop, uint32_t g) {
+  return drop != 0 && g == 1 && drop == (blockIdx.x == 0 ? DROP_OPERAND : blockIdx.x == 1 ? DROP_OPERAND_SECOND : -1);
 }
 
 // Before a CTA's shared memory is released: every commit to its barriers has arrived. Commits to different
 // barriers arrive in no stated order, so the last phase of each is waited for: `slices` commits went around
 // the ring, `accs` to the accumulators' barriers, one to `bar_last`.
 template <int NS>
-__device__ __forceinline__ void settle(uint32_t bar_empty, uint32_t slices, uint32_t bar_acc, uint32_t accs, uint32_t bar_last) {
+__device__ __forceinline__ void settle(uint32_t bar_empty, uint32_t slices, uint32_t bar_acc, uint32_t accs, uint32_t bar_last,
+                                       uint64_t limit) {
   for (uint32_t i = slices > NS ? slices - NS : 0; i < slices; ++i)
-    mbar_wait(bar_empty + 8 * (i % NS), (i / NS) & 1u, nullptr, kWaitLimitNs);
-  for (uint32_t i = accs > 2 ? accs - 2 : 0; i < accs; ++i) mbar_wait(bar_acc + 8 * (i & 1u), (i >> 1) & 1u, nullptr, kWaitLimitNs);
-  mbar_wait(bar_last, 0, nullptr, kWaitLimitNs);
+    mbar_wait(bar_empty + 8 * (i % NS), (i / NS) & 1u, nullptr, limit);
+  for (uint32_t i = accs > 2 ? accs - 2 : 0; i < accs; ++i) mbar_wait(bar_acc + 8 * (i & 1u), (i >> 1) & 1u, nullptr, limit);
+  mbar_wait(bar_last, 0, nullptr, limit);
 }
 
 // One 64-deep slice of an operand: `rows` rows along its M or N side, starting at r0, reduction from
@@ -396,13 +399,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int k = un.k_lo; k < un.k_hi; ++k, ++g) {
           const uint32_t s = g % C::NS;
           if (g >= C::NS) {
-            w = ring_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort);
+            w = mbar_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort, p.wait_limit_ns);
             if (w != WAIT_OK) break;
           }
           // rank 1's bytes may land first: its slice is free, so the barrier is already in this phase
           if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, CG * C::STAGE);
           const uint32_t dst = sb + s * C::STAGE;
           load_operand<CG, A_MN>(dst, &map_a, full0 + 8 * s, row0, BM, k * BK);
+          if (left_out(p.drop, g)) continue;
           load_operand<CG, B_MN>(dst + C::A_BYTES, &map_b, full0 + 8 * s, col0, C::B_ROWS, k * BK);
         }
       }
@@ -414,16 +418,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if constexpr (CG == 2) {
         if (rank == 1) send_counts(sb + C::OFF_COUNT, bar_count, 0, g, 0);
         mbar_arrive_expect_tx(bar_count, 8);
-        told = mbar_wait(bar_count, 0, nullptr, 2 * kWaitLimitNs) == WAIT_OK;
+        told = mbar_wait(bar_count, 0, nullptr, 2 * p.wait_limit_ns) == WAIT_OK;
       }
       if (rank == 0) {
         uint32_t last = g;
         // after an abort rank 1 may be ahead: slices that this CTA has not announced, with rank 1's bytes alone
         for (; told && last < s_count[0]; ++last) mbar_arrive_expect_tx(bar_full + 8 * (last % C::NS), C::STAGE);
         for (uint32_t i = last > C::NS ? last - C::NS : 0; i < last; ++i)
-          mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, kWaitLimitNs);
+          mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, p.wait_limit_ns);
       } else {
-        settle<C::NS>(bar_empty, told ? s_count[0] : 0u, bar_acc, told ? s_count[1] : 0u, bar_drain);
+        settle<C::NS>(bar_empty, told ? s_count[0] : 0u, bar_acc, told ? s_count[1] : 0u, bar_drain, p.wait_limit_ns);
       }
     }
   } else if (warp == 1) {
@@ -436,13 +440,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const Unit un = unit_of(p, t);
         const uint32_t acc = it & 1u;
         if (it >= 2) {
-          w = ring_wait(bar_free + 8 * acc, (it / 2 - 1u) & 1u, s_abort);
+          w = mbar_wait(bar_free + 8 * acc, (it / 2 - 1u) & 1u, s_abort, p.wait_limit_ns);
           if (w != WAIT_OK) break;
           tc_fence_after();
         }
         for (int k = un.k_lo; k < un.k_hi; ++k, ++g) {
           const uint32_t s = g % C::NS;
-          w = ring_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort);
+          w = mbar_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort, p.wait_limit_ns);
           if (w != WAIT_OK) break;
           tc_fence_after();
           const uint64_t da = da0 + ((s * C::STAGE) >> 4), db = db0 + ((s * C::STAGE) >> 4);
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_MMA);
       pair_commit<CG>(bar_drain);  // no MMA may be in flight when tensor memory is freed
       if constexpr (CG == 2) send_counts(sb + C::OFF_COUNT, bar_count, 1, g, done);
-      settle<C::NS>(bar_empty, g, bar_acc, done, bar_drain);
+      settle<C::NS>(bar_empty, g, bar_acc, done, bar_drain, p.wait_limit_ns);
     }
     __syncwarp();
   } else {
@@ -472,7 +476,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t free0 = CG == 1 ? bar_free : in_cta(bar_free, 0);
     const uint32_t bar_mine = bar_res + 16 * ew;
     uint32_t it = 0, chunks = 0, asked = 0;  // chunks stored; residual chunks asked for
-    for (int t = first; t < units; t += step, ++it) {
+    bool alive = true;  // no wait has expired
+    for (int t = first; t < units && alive; t += step, ++it) {
       const Unit un = unit_of(p, t);
       const int tm = un.tm, tn = un.tn;
       const uint32_t acc = it & 1u;
@@ -486,7 +491,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (pending == 0) bulk_wait_read<0>();
           else bulk_wait_read<1>();
           mbar_arrive_expect_tx(bar_mine + 8 * i, kEpiBuf);
-          tma_load_2d(buf0 + i * kEpiBuf, &map_res, bar_mine + 8 * i, col, row0);
+          if (p.drop != DROP_RESIDUAL || asked != (TN > 64 ? 1u : 0u) || blockIdx.x != 0 || ew != 0)
+            tma_load_2d(buf0 + i * kEpiBuf, &map_res, bar_mine + 8 * i, col, row0);
         }
         ++asked;
       };
@@ -502,11 +508,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
       for (int j = 0; j < 8; ++j) bias[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (p.bias != nullptr) read_bias(c_lo);
-      const int w = ring_wait(bar_acc + 8 * acc, (it / 2) & 1u, s_abort);
+      const int w = mbar_wait(bar_acc + 8 * acc, (it / 2) & 1u, s_abort, p.wait_limit_ns);
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
       if (__any_sync(0xffffffffu, w != WAIT_OK)) {
-        // a copy of the residual's must not outlive the buffer
-        if (asked != chunks && with_res) mbar_wait(bar_mine + 8 * (chunks & 1u), (chunks >> 1) & 1u, nullptr, kWaitLimitNs);
+        alive = false;
         break;
       }
       tc_fence_after();
@@ -568,8 +573,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (with_res) {
           if (c + 32 < c_lo + TN / 2 && col0 + 32 < p.No) ask(col0 + 32, 0);
           const uint32_t i = chunks & 1u;
-          const int rw = ring_wait(bar_mine + 8 * i, (chunks >> 1) & 1u, s_abort);
+          const int rw = mbar_wait(bar_mine + 8 * i, (chunks >> 1) & 1u, s_abort, p.wait_limit_ns);
           if (rw == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
+          if (__any_sync(0xffffffffu, rw != WAIT_OK)) {  // the buffer does not hold the residual
+            alive = false;
+            break;
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -594,12 +603,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         emit(&map_out);
         ++chunks;
       }
+      if (!alive) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if constexpr (CG == 1) mbar_arrive(bar_free + 8 * acc);
         else mbar_arrive_cluster(free0 + 8 * acc);
       }
+    }
+    // after an abort: a copy of the residual's must not outlive its buffer
+    if (!alive && p.has_residual) {
+      for (uint32_t n = chunks; n != asked; ++n) mbar_wait(bar_mine + 8 * (n & 1u), (n >> 1) & 1u, nullptr, p.wait_limit_ns);
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -710,6 +724,8 @@ struct FewParams {
   __nv_bfloat16* out;
   __nv_bfloat16* z;
   int act;
+  int drop;
+  uint64_t wait_limit_ns;
   uint32_t* ws;
 };
 
@@ -758,16 +774,17 @@ __global__ void __launch_bounds__(kFewThreads)
       for (int k = k_lo; k < k_hi; ++k, ++g) {
         const uint32_t s = g % C::NS;
         if (g >= C::NS) {
-          w = ring_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort);
+          w = mbar_wait(bar_empty + 8 * s, (g / C::NS - 1u) & 1u, s_abort, p.wait_limit_ns);
           if (w != WAIT_OK) break;
         }
         mbar_arrive_expect_tx(bar_full + 8 * s, C::STAGE);
         tma_load_2d(sb + s * C::STAGE, &map_w, bar_full + 8 * s, k * BK, n0);
+        if (left_out(p.drop, g)) continue;
         tma_load_2d(sb + s * C::STAGE + C::A_BYTES, &map_x, bar_full + 8 * s, k * BK, 0);
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_PRODUCER);
       for (uint32_t i = g > C::NS ? g - C::NS : 0; i < g; ++i)
-        mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, kWaitLimitNs);
+        mbar_wait(bar_full + 8 * (i % C::NS), (i / C::NS) & 1u, nullptr, p.wait_limit_ns);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -778,7 +795,7 @@ __global__ void __launch_bounds__(kFewThreads)
       int w = WAIT_OK;
       for (int k = k_lo; k < k_hi; ++k, ++g) {
         const uint32_t s = g % C::NS;
-        w = ring_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort);
+        w = mbar_wait(bar_full + 8 * s, (g / C::NS) & 1u, s_abort, p.wait_limit_ns);
         if (w != WAIT_OK) break;
         tc_fence_after();
         const uint64_t da = da0 + ((s * C::STAGE) >> 4), db = db0 + ((s * C::STAGE) >> 4);
@@ -789,11 +806,11 @@ __global__ void __launch_bounds__(kFewThreads)
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_MMA);
       tc_commit(bar_acc);  // also after an abort: the MMAs in flight end before tensor memory is freed
-      settle<C::NS>(bar_empty, g, bar_acc, 0, bar_acc);
+      settle<C::NS>(bar_empty, g, bar_acc, 0, bar_acc, p.wait_limit_ns);
     }
     __syncwarp();
   } else {
-    const int w = ring_wait(bar_acc, 0, nullptr);
+    const int w = mbar_wait(bar_acc, 0, nullptr, p.wait_limit_ns);
     if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
     ok = !__any_sync(0xffffffffu, w != WAIT_OK);
     if (ok) {
@@ -1041,6 +1058,8 @@ cudaError_t launch_linear_gemm(const GemmArgs& a, cudaStream_t stream) {
   p.act = a.act;
   p.store_z = a.z != nullptr;
   p.part = a.part;
+  p.drop = a.drop;
+  p.wait_limit_ns = a.wait_limit_ns;
   p.ws = a.ws;
   if (a.a_mn) return launch_gemm_n<true, true>(a, p, stream);
   return a.b_mn ? launch_gemm_n<false, true>(a, p, stream) : launch_gemm_n<false, false>(a, p, stream);
@@ -1056,6 +1075,8 @@ cudaError_t launch_linear_few(const FewArgs& a, cudaStream_t stream) {
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.z = static_cast<__nv_bfloat16*>(a.z);
   p.act = a.act;
+  p.drop = a.drop;
+  p.wait_limit_ns = a.wait_limit_ns;
   p.ws = a.ws;
   // the reduction over 1, 2, 4 or 8 CTAs: as many as are resident at once, each with two slices at least
   // (2 x 5120 -> 30720: 49.7 us over 2, 52.2 over 4; 16 x 4096 -> 4096: 17.3, 12.2 and 11.0 over 2, 4, 8)

@@ -17,7 +17,7 @@
 namespace {
 
 thread_local std::string g_last_error;
-int g_drop_one_load = 0;  // failure-detection test hook, consumed by the next bf16 launch
+int g_drop_one_load = 0;  // failure-detection test hook, consumed by the next launch that it is for
 unsigned long long* g_cta_times = nullptr;  // measurement hook, consumed by the next bf16 launch
 int g_cta_capacity = 0;
 
@@ -40,6 +40,14 @@ sol_status fail(sol_status s, const char* fmt, ...) {
 
 sol_status cuda_fail(cudaError_t e, const char* what) {
   return fail(SOL_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+int take_drop(bool linear, uint64_t* wait_limit_ns) {
+  const bool mine = g_drop_one_load != 0 && (g_drop_one_load >= sol::DROP_OPERAND) == linear;
+  *wait_limit_ns = mine ? 200000000ull : 2000000000ull;
+  const int drop = mine ? g_drop_one_load : 0;
+  if (mine) g_drop_one_load = 0;
+  return drop;
 }
 
 // Device checks: an sm_100 GPU is current. Returns SOL_OK and its SM count, which a device keeps: it is
@@ -444,9 +452,7 @@ sol_status fwd_impl(const void* Q, const void* K, const void* V, const float* kb
   a.k_keep = k_keep;
 
   if (bf16) {
-    a.drop_one_load = g_drop_one_load;
-    if (g_drop_one_load) a.wait_limit_ns = 200000000ull;
-    g_drop_one_load = 0;
+    a.drop_one_load = take_drop(false, &a.wait_limit_ns);
     a.cta_times = g_cta_times;
     a.cta_capacity = g_cta_capacity;
     g_cta_times = nullptr;

@@ -478,8 +478,11 @@ sol_status sol_attn_linear_bwd(const void* dy, const void* x, const void* w, con
 /* Test hook for the failure-detection path. mode 0 (default) = normal operation. mode 1 makes
  * the next sol_attn_fwd launch (SOL_BF16 path) skip one K-tile load, so the consumer's bounded
  * wait expires: the launch returns early, sets the device error word, and
- * sol_attn_check_device_error then reports SOL_ETIMEOUT. The hook applies to one launch and
- * then resets to 0. The wait limit is about 0.2 s in that mode and about 2 s otherwise. */
+ * sol_attn_check_device_error then reports SOL_ETIMEOUT. Modes 2, 3 and 4 do the same to the next
+ * product of sol_attn_linear or sol_attn_linear_bwd: its first (2) or second (3) CTA skips a slice of an
+ * operand, where its reduction has two (more than 64 deep), or its first a chunk of the residual (4, more than
+ * 128 rows). The hook applies to one launch and then resets to 0. The wait limit is about 0.2 s in
+ * that mode and about 2 s otherwise. */
 void sol_attn_debug_drop_one_load(int mode);
 
 /* Measurement hook for the persistent scheduler's load balance. The next sol_attn_fwd launch of
