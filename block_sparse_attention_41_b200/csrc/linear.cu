@@ -27,7 +27,8 @@
 // so no workspace and no atomics are needed and the bits do not depend on timing.
 //
 // Every wait is bounded: on expiry the CTA records the timeout in the caller's workspace (where one
-// is given), lets its copies and MMAs in flight end, frees its tensor memory and returns.
+// is given), lets its copies and MMAs in flight end, frees its tensor memory and returns. What it could not
+// compute it stores as NaN, also in what other CTAs add to theirs, so that the data tell without a workspace.
 #include <cmath>
 #include <type_traits>
 
@@ -340,6 +341,12 @@ __device__ __forceinline__ Unit unit_of(const GemmParams& p, int u) {
   return w;
 }
 
+// Where unit `u`, a piece, keeps the 32 x 32 sums of CTA `rank`, TMEM lanes 32 q.. and columns c..: 8 x 32 vectors.
+template <int CG, int TN>
+__device__ __forceinline__ float4* piece_chunk(const GemmParams& p, int u, uint32_t rank, int q, int c) {
+  return reinterpret_cast<float4*>(p.part) + (((static_cast<size_t>(u - p.whole) * CG + rank) * 4 + q) * (TN / 32) + c / 32) * 256;
+}
+
 // ---- many rows ------------------------------------------------------------------------------------
 template <int CG, int TN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
@@ -477,7 +484,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t bar_mine = bar_res + 16 * ew;
     uint32_t it = 0, chunks = 0, asked = 0;  // chunks stored; residual chunks asked for
     bool alive = true;  // no wait has expired
-    for (int t = first; t < units && alive; t += step, ++it) {
+    int t = first, undone = c_lo;  // the unit at hand; after an abort the first column of it that has not left
+    for (; t < units; t += step, ++it) {
       const Unit un = unit_of(p, t);
       const int tm = un.tm, tn = un.tn;
       const uint32_t acc = it & 1u;
@@ -522,8 +530,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t r[32];
         tmem_ld_x32(tmem + lane_base + acc * TN + c, r);
         if (t >= p.whole) {  // a piece: its sums as they are, 16 bytes per lane side by side, for the kernel that adds them
-          float4* to = reinterpret_cast<float4*>(p.part) +
-                       (((static_cast<size_t>(t - p.whole) * CG + rank) * 4 + q) * (TN / 32) + c / 32) * 256 + lane;
+          float4* to = piece_chunk<CG, TN>(p, t, rank, q, c) + lane;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             to[32 * j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
@@ -577,6 +584,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (rw == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
           if (__any_sync(0xffffffffu, rw != WAIT_OK)) {  // the buffer does not hold the residual
             alive = false;
+            undone = c;
             break;
           }
 #pragma unroll
@@ -611,9 +619,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         else mbar_arrive_cluster(free0 + 8 * acc);
       }
     }
-    // after an abort: a copy of the residual's must not outlive its buffer
-    if (!alive && p.has_residual) {
-      for (uint32_t n = chunks; n != asked; ++n) mbar_wait(bar_mine + 8 * (n & 1u), (n >> 1) & 1u, nullptr, p.wait_limit_ns);
+    if (!alive) {
+      // a copy of the residual's must not outlive its buffer
+      if (p.has_residual) {
+        for (uint32_t n = chunks; n != asked; ++n) mbar_wait(bar_mine + 8 * (n & 1u), (n >> 1) & 1u, nullptr, p.wait_limit_ns);
+      }
+      // NaN to all that is left of this warp's outputs, or pieces
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+      for (int j = 0; j < 4; ++j)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(buf0 + lane * 64 + 16 * j), "r"(0x7fff7fffu) : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      for (; t < units; t += step, undone = c_lo) {
+        const Unit un = unit_of(p, t);
+        const int row0 = (un.tm * CG + static_cast<int>(rank)) * BM + q * 32;
+        for (int c = undone; c < c_lo + TN / 2 && un.tn * TN + c < p.No; c += 32) {
+          if (t >= p.whole) {
+            float4* to = piece_chunk<CG, TN>(p, t, rank, q, c) + lane;
+            const float n = __uint_as_float(0x7fffffffu);
+            for (int j = 0; j < 8; ++j) to[32 * j] = make_float4(n, n, n, n);
+          } else if (lane == 0 && row0 < p.Mo) {
+            tma_store_2d(&map_out, buf0, un.tn * TN + c, row0);
+            if (p.store_z) tma_store_2d(&map_z, buf0, un.tn * TN + c, row0);
+            bulk_commit();
+          }
+        }
+      }
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -766,7 +798,6 @@ __global__ void __launch_bounds__(kFewThreads)
   const uint32_t tmem = *s_tmem;
   chained_wait();
 
-  bool ok = true;  // of the epilogue warps: the accumulator is complete
   if (warp == 0) {
     if (lane == 0) {
       uint32_t g = 0;
@@ -812,8 +843,7 @@ __global__ void __launch_bounds__(kFewThreads)
   } else {
     const int w = mbar_wait(bar_acc, 0, nullptr, p.wait_limit_ns);
     if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_SOFTMAX);
-    ok = !__any_sync(0xffffffffu, w != WAIT_OK);
-    if (ok) {
+    if (!__any_sync(0xffffffffu, w != WAIT_OK)) {
       tc_fence_after();
       // every slice has been read by the MMAs, so the partial tile may take the ring's place
       const int q = warp & 3, n = q * 32 + lane;
@@ -832,11 +862,15 @@ __global__ void __launch_bounds__(kFewThreads)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
-  const bool aborted = *s_abort != 0;
+  if (*s_abort != 0) {  // the partial tile is incomplete: NaN, which the sums over the cluster keep
+    const float n = __uint_as_float(0x7fffffffu);
+    for (int e = tid; e < p.M * (BM / 4); e += kFewThreads) reinterpret_cast<float4*>(smem)[e] = make_float4(n, n, n, n);
+    __syncthreads();
+  }
   if (p.split > 1) cluster_arrive_wait();
   // each CTA of the cluster finishes an equal share of the M x 128 values, four at a time (128 / 4 is a
   // multiple of split)
-  if (!aborted) {
+  {
     const int share = p.M * (BM / 4) / p.split;
     for (int e = rank * share + tid; e < (rank + 1) * share; e += kFewThreads) {
       const int m = e / (BM / 4), n = n0 + 4 * (e & (BM / 4 - 1));

@@ -449,9 +449,10 @@ typedef enum { SOL_ACT_NONE = 0, SOL_ACT_GELU = 1, SOL_ACT_GELU_TANH = 2, SOL_AC
  *   act        gelu: z Phi(z); gelu_tanh: its tanh form; silu: z / (1 + exp(-z))
  *   out        device, out, bf16 [M, N]; may be residual itself
  *   z          device, out, bf16 [M, N], or NULL: what sol_attn_linear_bwd needs of an activation
- *   workspace  device, or NULL. Its first 256 bytes, zeroed once, are for sol_attn_check_device_error;
- *              without them an expired device wait leaves out incomplete and unreported. With
+ *   workspace  device, or NULL. Its first 256 bytes, zeroed once, are for sol_attn_check_device_error. With
  *              sol_attn_linear_workspace_bytes(...) bytes, a product of few tiles is split along K
+ * After an expired device wait, with a workspace or without, what was not computed of out and z is NaN (and so of
+ * the gradients below).
  * N and K in multiples of 8, any M from 1. Up to 128 rows run on a kernel of their own; its sums, and those
  * of a split product, may differ from the others' in the last bit, as fp32 sums in another order do. */
 size_t sol_attn_linear_workspace_bytes(int M, int N, int K); /* 0 for sizes that sol_attn_linear refuses */

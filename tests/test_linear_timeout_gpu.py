@@ -101,3 +101,58 @@ def test_a_lost_operand_of_a_gradient_is_reported(M, N, K, which, mode):
     got = call()
     assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
     sa.sol_attn_check_device_error(ws)
+
+
+def right_or_nan(got, want, what):
+    """Every value is the healthy call's or NaN, and some are NaN."""
+    nan = got.isnan()
+    assert bool(nan.any()), what
+    bad = ~(nan | (got == want))
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} wrong values, the first at {bad.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("mode", [FIRST, SECOND])
+@pytest.mark.parametrize("act", ["none", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M,N,K", FEW + ONE + PAIRS + SPLIT)
+def test_what_a_lost_operand_leaves_is_nan(M, N, K, act, mode):
+    """On the default path, without error words, on outputs and a workspace that held other values before."""
+    x, w, res = operands(M, N, K)
+    bias = torch.arange(N, device="cuda").remainder(5).float()
+    w = (w.float() / 64).to(BF)
+    want, zz = sa.sol_attn_linear(x, w, bias, act, res, want_z=True)
+    out, z = torch.full_like(want, 7.0), torch.full_like(want, 7.0)
+    sa.sol_attn_debug_drop_one_load(mode)
+    sa.sol_attn_linear(x, w, bias, act, res, out=out, z=z)
+    torch.cuda.synchronize()
+    right_or_nan(out, want, "out")
+    right_or_nan(z, zz, "z")
+    assert torch.equal(out.isnan(), z.isnan())
+    again, za = sa.sol_attn_linear(x, w, bias, act, res, want_z=True)
+    assert torch.equal(again, want) and torch.equal(za, zz)
+
+
+@pytest.mark.parametrize("M,N,K", ONE + PAIRS)
+def test_what_a_lost_residual_leaves_is_nan(M, N, K):
+    x, w, res = operands(M, N, K)
+    want, zz = sa.sol_attn_linear(x, w, residual=res, want_z=True)
+    out, z = torch.full_like(want, 7.5), torch.full_like(want, 7.5)
+    sa.sol_attn_debug_drop_one_load(RESIDUAL)
+    sa.sol_attn_linear(x, w, residual=res, out=out, z=z)
+    torch.cuda.synchronize()
+    right_or_nan(out, want, "out")
+    right_or_nan(z, zz, "z")
+
+
+@pytest.mark.parametrize("mode", [FIRST, SECOND])
+@pytest.mark.parametrize("which", ["dx", "dw"])
+@pytest.mark.parametrize("M,N,K", [(300, 264, 136), (4104, 4096, 136), (1000, 1024, 1024)])
+def test_what_a_lost_operand_of_a_gradient_leaves_is_nan(M, N, K, which, mode):
+    x, w, dy = operands(M, N, K)
+
+    def call():
+        dx, dw, _ = sa.sol_attn_linear_bwd(dy, x, w, want_dx=which == "dx", want_dw=which == "dw", want_db=False)
+        return dx if which == "dx" else dw
+    want = call()
+    sa.sol_attn_debug_drop_one_load(mode)
+    right_or_nan(call(), want, which)
+    assert torch.equal(call(), want)
