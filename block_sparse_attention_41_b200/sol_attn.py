@@ -604,8 +604,8 @@ class _On:
         index = self.device.index
         if self.stream is not None:
             s = self.stream
-            if not hasattr(s, "cuda_stream"):
-                s = torch.cuda.ExternalStream(int(s), device=self.device)
+            if not hasattr(s, "cuda_stream"):  # a handle; torch takes 0, the default stream's, for a wish for a new stream
+                s = torch.cuda.ExternalStream(int(s), device=self.device) if int(s) else torch.cuda.default_stream(self.device)
             elif s.device != self.device:
                 raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
             self._contexts = (torch.cuda.stream(s),)
