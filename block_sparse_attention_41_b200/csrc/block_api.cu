@@ -315,6 +315,7 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
       !aligned_to(pos, 4) || !aligned_to(inv_freq, 8))
     return fail(SOL_EINVAL, "device pointers must be aligned to their elements");
   if (d > 512 || d % 2 != 0) return fail(SOL_EUNSUPPORTED, "rotary positions need an even d <= 512 (d=%d)", d);
+  if (B > 1 && pos_stride_b < 0) return fail(SOL_EINVAL, "pos_stride_b=%lld must not be negative", static_cast<long long>(pos_stride_b));
   if (B > 65535 || static_cast<long long>(Hq) + Hk > 65535) return fail(SOL_EUNSUPPORTED, "B and Hq + Hk must be <= 65535");
   const int esize = dt == SOL_BF16 ? 2 : 4;
   a.width = 16 / esize;

@@ -429,7 +429,7 @@ sol_status sol_attn_rope_tables(const int32_t* pos, int axes, const int* section
  *   Q_out, K_out device, out, same shapes, strides of their own (at least d). In place (the same
  *                pointer) the strides must agree. Token-major projections in, head-major tensors
  *                out, or back for a gradient, need no copy of their own
- *   pos          device, int32 [axes, L] per batch entry, pos_stride_b elements apart (0: shared)
+ *   pos          device, int32 [axes, L] per batch entry, pos_stride_b >= 0 elements apart (0: shared)
  *   sections, inv_freq, attn_factor as above
  * Even d <= 512, any even rot <= d. Accesses of 16 bytes where addresses, strides, d and (half layout)
  * rot / 2 allow them, else of 8, 4 or single values. B <= 65535, Hq + Hk <= 65535. */
