@@ -1,6 +1,7 @@
 // C ABI of the dense operators around the attention (declared in include/sol_attn.h): gated
 // residual and norm, rotary positions, linear layer. Arguments are checked on the host before anything is
 // launched; nothing here allocates device memory.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -89,6 +90,34 @@ sol_status rope_sections(int rot, int axes, const int* sections, int (&end)[4]) 
   return SOL_OK;
 }
 
+// Do the rows of d values of an output lie apart? Strides of sizes above one have to nest: from the shortest on,
+// each is at least as long as everything within it.
+bool rows_apart(const int (&sizes)[3], const int64_t* strides, int d) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int i, int j) { return strides[i] < strides[j]; });
+  __int128 extent = d;
+  for (int i : order) {
+    if (sizes[i] == 1) continue;
+    if (strides[i] < extent) return false;
+    extent += static_cast<__int128>(strides[i]) * (sizes[i] - 1);
+  }
+  return true;
+}
+
+// Is one of the outputs given twice, or also as one of the inputs that other blocks still read? (Null: not there.
+// The starts are compared: the same buffer given twice is what happens by mistake.)
+template <size_t O, size_t I>
+bool shares(const void* const (&outs)[O], const void* const (&ins)[I]) {
+  for (size_t i = 0; i < O; ++i) {
+    if (outs[i] == nullptr) continue;
+    for (size_t j = 0; j < i; ++j)
+      if (outs[i] == outs[j]) return true;
+    for (const void* in : ins)
+      if (outs[i] == in) return true;
+  }
+  return false;
+}
+
 // 2-D bf16 view [rows][inner] with boxes of box_inner x box_rows; what lies outside reads as zero and
 // is not written.
 sol_status make_map2d(CUtensorMap* m, const void* base, int inner, int rows, int box_inner, int box_rows,
@@ -163,6 +192,7 @@ sol_status sol_attn_residual_norm(const void* x, const void* y, const float* gat
   if (st != SOL_OK) return st;
   if (h == nullptr || (y != nullptr) != (x_out != nullptr))
     return fail(SOL_EINVAL, "h must be non-null, and x_out given exactly where y is");
+  if (x_out == h) return fail(SOL_EINVAL, "x_out and h must be two buffers");
   if (!aligned16(h) || !aligned16(x_out)) return fail(SOL_EINVAL, "x_out and h must be 16-byte aligned");
   int sms = 0;
   if ((st = current_device(&sms)) != SOL_OK) return st;
@@ -192,6 +222,7 @@ sol_status sol_attn_residual_norm_bwd(const void* dh, const void* dx_out, const 
   if (dh == nullptr || dx == nullptr || (y != nullptr) != (dy != nullptr))
     return fail(SOL_EINVAL, "dh and dx must be non-null, and dy given exactly where y is");
   if (dx_out != nullptr && y == nullptr) return fail(SOL_EINVAL, "dx_out needs y: without a residual step there is no x_out");
+  if (dx == dy) return fail(SOL_EINVAL, "dx and dy must be two buffers");
   const void* ptrs[] = {dh, dx_out, dx, dy, workspace};
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return fail(SOL_EINVAL, "device pointers must be 16-byte aligned");
@@ -310,6 +341,8 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
     return fail(SOL_EINVAL, "Q, Q_out, their strides, pos and inv_freq must be non-null");
   if (Hk > 0 && (K == nullptr || K_out == nullptr || k_strides == nullptr || k_out_strides == nullptr))
     return fail(SOL_EINVAL, "K, K_out and their strides must be non-null for Hk > 0");
+  if (Hk > 0 && (Q_out == K_out || Q_out == K || K_out == Q))
+    return fail(SOL_EINVAL, "an output must be neither the other side's input nor its output");
   const size_t es = dt == SOL_BF16 ? 2 : 4;
   if (!aligned_to(Q, es) || !aligned_to(Q_out, es) || (Hk > 0 && (!aligned_to(K, es) || !aligned_to(K_out, es))) ||
       !aligned_to(pos, 4) || !aligned_to(inv_freq, 8))
@@ -347,6 +380,7 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
       narrow_to(in[k]);
       narrow_to(out[k]);
     }
+    if (!rows_apart(sizes, out, d)) return fail(SOL_EINVAL, "rows of an output overlap: strides must nest");
     if (r.in == r.out && !same) return fail(SOL_EINVAL, "in place, input and output must have the same strides");
     if (!same) a.copy_rest = true;
     narrow_to(static_cast<long long>(reinterpret_cast<uintptr_t>(r.in) % 16) / esize);
@@ -386,6 +420,10 @@ sol_status sol_attn_linear(const void* x, const void* w, const float* bias, cons
   sol_status st = linear_sizes(M, N, K, act);
   if (st != SOL_OK) return st;
   if (x == nullptr || w == nullptr || out == nullptr) return fail(SOL_EINVAL, "x, w and out must be non-null");
+  const void* const outs[] = {out, z};
+  const void* const ins[] = {x, w, workspace};
+  if (shares(outs, ins) || (z != nullptr && z == residual))
+    return fail(SOL_EINVAL, "out and z must be two buffers, neither of them x, w or the workspace, nor z the residual");
   const void* ptrs[] = {x, w, bias, residual, out, z, workspace};
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return fail(SOL_EINVAL, "device pointers must be 16-byte aligned");
@@ -443,6 +481,9 @@ sol_status sol_attn_linear_bwd(const void* dy, const void* x, const void* w, con
   if (dx != nullptr && w == nullptr) return fail(SOL_EINVAL, "dx needs w");
   if (dw != nullptr && x == nullptr) return fail(SOL_EINVAL, "dw needs x");
   if ((act != SOL_ACT_NONE) != (z != nullptr)) return fail(SOL_EINVAL, "z must be given exactly where there is an activation");
+  const void* const outs[] = {dx, dw, db};
+  const void* const ins[] = {dy, x, w, z, workspace};
+  if (shares(outs, ins)) return fail(SOL_EINVAL, "dx, dw and db must be buffers of their own");
   const void* ptrs[] = {dy, x, w, z, dx, dw, workspace};
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return fail(SOL_EINVAL, "device pointers must be 16-byte aligned");

@@ -341,7 +341,8 @@ sol_status sol_attn_fwd_host(const void* Q, const void* K, const void* V, void* 
  * kernel fusion of the memory-bound DiT glue; the review page of the Sol Video Inference Engine
  * paper names GEMM+GELU, GEMM+residual, fused RoPE+norm and fused AdaLN) and print no formulas; the
  * definitions below are this library's. They follow the conventions above; where a call accepts
- * strides or smaller alignments, it says so. Outputs must not overlap inputs unless stated. */
+ * strides or smaller alignments, it says so. Outputs must not overlap inputs unless stated, nor one another; the
+ * same buffer in two such places is refused. */
 
 typedef enum { SOL_NORM_NONE = 0, SOL_NORM_LAYER = 1, SOL_NORM_RMS = 2 } sol_norm;
 
@@ -426,7 +427,8 @@ sol_status sol_attn_rope_tables(const int32_t* pos, int axes, const int* section
  *   Q, K         device, [B, Hq, L, d] and [B, Hk, L, d] in dtype `dt`, with strides (in elements)
  *                q_strides = {b, h, l} on the HOST, channels contiguous; strides may be 0 (shared).
  *                Hk = 0: no keys
- *   Q_out, K_out device, out, same shapes, strides of their own (at least d). In place (the same
+ *   Q_out, K_out device, out, same shapes, strides of their own that nest, so that no two rows overlap (the
+ *                shortest at least d, each other one at least what lies within it). In place (the same
  *                pointer) the strides must agree. Token-major projections in, head-major tensors
  *                out, or back for a gradient, need no copy of their own
  *   pos          device, int32 [axes, L] per batch entry, pos_stride_b >= 0 elements apart (0: shared)
