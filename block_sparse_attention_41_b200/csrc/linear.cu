@@ -142,10 +142,12 @@ __device__ __forceinline__ f2 activation_slope(f2 z) {
     const f2 c = normal_cdf(z, e);
     return fma2(mul2(z, dup2(0.39894228040143268f)), e, c);
   } else if constexpr (ACT == ACT_GELU_TANH) {
-    const f2 z2 = mul2(z, z), s = sigmoid_ex2(gelu_tanh_arg(z, z2));
-    // s + z s (1 - s) 2 sqrt(2 / pi) (1 + 3 0.044715 z^2)
-    const f2 g = mul2(z, fma2(z2, dup2(1.5957691216057308f * 3.0f * 0.044715f), dup2(1.5957691216057308f)));
-    return fma2(mul2(g, s), fma2(s, dup2(-1.0f), dup2(1.0f)), s);
+    // s + z s (1 - s) 2 sqrt(2 / pi) (1 + 3 0.044715 z^2). Beyond |z| = 100, s is 0 or 1 and its product with 1 - s 0:
+    // the cubic stays finite there, so that the slope does, up to the largest z
+    const float2 q = unpack2(mul2(z, z));
+    const f2 z2 = pack2(fminf(q.x, 1e4f), fminf(q.y, 1e4f)), s = sigmoid_ex2(gelu_tanh_arg(z, z2));
+    const f2 g = mul2(z, mul2(s, fma2(s, dup2(-1.0f), dup2(1.0f))));
+    return fma2(g, fma2(z2, dup2(1.5957691216057308f * 3.0f * 0.044715f), dup2(1.5957691216057308f)), s);
   } else if constexpr (ACT == ACT_SILU) {
     const f2 s = sigmoid_ex2(mul2(z, dup2(-1.4426950408889634f)));
     return mul2(s, fma2(z, fma2(s, dup2(-1.0f), dup2(1.0f)), dup2(1.0f)));
