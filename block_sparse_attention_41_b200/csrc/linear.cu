@@ -281,9 +281,9 @@ constexpr uint32_t instr_desc(int M, int N, bool a_mn, bool b_mn) {
   return idesc_bf16_f32(M, N, b_mn) | (a_mn ? 1u << 15 : 0u);
 }
 
-// For the tests of expired waits: does this CTA leave out its copy of an operand's slice `g`?
-__device__ __forceinline__ bool left_out(int drop, uint32_t g) {
-  return drop != 0 && g == 1 && drop == (blockIdx.x == 0 ? DROP_OPERAND : blockIdx.x == 1 ? DROP_OPERAND_SECOND : -1);
+// For the tests of expired waits: the slice of an operand whose copy this CTA leaves out, if any.
+__device__ __forceinline__ uint32_t left_out(int drop) {
+  return drop == (blockIdx.x == 0 ? DROP_OPERAND : blockIdx.x == 1 ? DROP_OPERAND_SECOND : -1) ? 1u : ~0u;
 }
 
 // Before a CTA's shared memory is released: every commit to its barriers has arrived. Commits to different
@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tma_prefetch_desc(&map_a);
       tma_prefetch_desc(&map_b);
       const uint32_t full0 = CG == 1 ? bar_full : in_cta(bar_full, 0);
+      const uint32_t gone = left_out(p.drop);
       uint32_t g = 0;  // slices loaded so far
       int w = WAIT_OK;
       for (int t = first; t < units && w == WAIT_OK; t += step) {
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, CG * C::STAGE);
           const uint32_t dst = sb + s * C::STAGE;
           load_operand<CG, A_MN>(dst, &map_a, full0 + 8 * s, row0, BM, k * BK);
-          if (left_out(p.drop, g)) continue;
+          if (g == gone) continue;
           load_operand<CG, B_MN>(dst + C::A_BYTES, &map_b, full0 + 8 * s, col0, C::B_ROWS, k * BK);
         }
       }
@@ -802,6 +803,7 @@ __global__ void __launch_bounds__(kFewThreads)
 
   if (warp == 0) {
     if (lane == 0) {
+      const uint32_t gone = left_out(p.drop);
       uint32_t g = 0;
       int w = WAIT_OK;
       for (int k = k_lo; k < k_hi; ++k, ++g) {
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(kFewThreads)
         }
         mbar_arrive_expect_tx(bar_full + 8 * s, C::STAGE);
         tma_load_2d(sb + s * C::STAGE, &map_w, bar_full + 8 * s, k * BK, n0);
-        if (left_out(p.drop, g)) continue;
+        if (g == gone) continue;
         tma_load_2d(sb + s * C::STAGE + C::A_BYTES, &map_x, bar_full + 8 * s, k * BK, 0);
       }
       if (w == WAIT_TIMEOUT) report(s_abort, p.ws, WHERE_PRODUCER);
