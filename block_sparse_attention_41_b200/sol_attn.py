@@ -772,8 +772,9 @@ def sol_attn_rope_inv_freq(rot: int, base: float = 10000.0, sections=None, scali
 def _check_positions(pos, inv_freq, sections, device, L: int, B: Optional[int]):
     """(axes, sections array, stride of a batch entry's positions)."""
     axes = len(sections) if sections is not None else 1
-    if not (_fits(pos, device.index, torch.int32, (axes, L)) and inv_freq.get_device() == device.index and
-            inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+    if not (_fits(pos, device.index, torch.int32, (axes, L)) and isinstance(inv_freq, torch.Tensor) and
+            inv_freq.get_device() == device.index and inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and
+            inv_freq.is_contiguous()):
         _need_cuda_on("pos", pos, device, torch.int32)
         _need_cuda_on("inv_freq", inv_freq, device, torch.float64)
         if not pos.is_contiguous() or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
@@ -861,19 +862,18 @@ def sol_attn_rope(Q, K, pos, inv_freq, layout: str = "interleaved", sections=Non
     return Q_out, K_out
 
 
-def _check_linear(first: str, a, w, x=None):
-    """Shapes of a product's bf16 operands: leading shape, M, N, K. `a` is x or, with x given apart, dy."""
+def _check_linear(**operands):
+    """A product's bf16 operands by name, w among them: contiguous, on the device of the first."""
+    a = next(iter(operands.values()))
     if not isinstance(a, torch.Tensor) or not a.is_cuda:
-        raise TypeError(f"{first} must be a CUDA tensor")
+        raise TypeError(f"{next(iter(operands))} must be a CUDA tensor")
     index = a.get_device()
-    for n, t in ((first, a), ("w", w), ("x", x)):
-        if t is None:
-            continue
+    for n, t in operands.items():
         if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype is not _BF16:
             _need_cuda_on(n, t, a.device, _BF16)
         if not t.is_contiguous() or t.dim() < 1:
             raise ValueError(f"{n} must be contiguous")
-    if w is not None and w.dim() != 2:
+    if operands["w"].dim() != 2:
         raise ValueError("w must be [N, K]")
 
 
@@ -891,7 +891,7 @@ def sol_attn_linear(x, w, bias=None, act: str = "none", residual=None, out=None,
     sol_attn_linear_bwd) when want_z or a z tensor is given. workspace: a uint8 tensor whose first 256 bytes
     are zeroed, for sol_attn_check_device_error; with sol_attn_linear_workspace_bytes bytes (the default)
     a product of few tiles is split along K."""
-    _check_linear("x", x, w)
+    _check_linear(x=x, w=w)
     code = _choice("act", act, ACTIVATIONS)
     N, K = w.shape
     if x.shape[-1] != K:
@@ -932,7 +932,7 @@ def sol_attn_linear_bwd(dy, x, w, z=None, act: str = "none", want_dx: bool = Tru
                         want_db: bool = True, workspace=None, stream=None):
     """Gradients of sol_attn_linear from dy bf16 [..., N], its inputs and, with an activation, the z that it
     returned. Returns (dx, dw, db), bf16, bf16 and fp32, None where not wanted; residual's is dy."""
-    _check_linear("dy", dy, w, x)
+    _check_linear(dy=dy, w=w, x=x)
     code = _choice("act", act, ACTIVATIONS)
     N, K = w.shape
     if dy.shape[-1] != N or x.shape != dy.shape[:-1] + (K,):
