@@ -313,7 +313,6 @@ sol_status sol_attn_rope_tables(const int32_t* pos, int axes, const int* section
   a.inv_freq = inv_freq;
   a.L = L;
   a.rot = rot;
-  a.axes = axes;
   a.factor = attn_factor;
   a.cos = rope_cos;
   a.sin = rope_sin;
@@ -395,7 +394,6 @@ sol_status sol_attn_rope(const void* Q, const int64_t* q_strides, const void* K,
   a.L = L;
   a.d = d;
   a.rot = rot;
-  a.axes = axes;
   a.factor = attn_factor;
   a.half = layout == SOL_ROPE_HALF;
   a.inverse = inverse != 0;

@@ -167,7 +167,7 @@ struct RopeArgs {
   const int* pos;        // [axes, L], pos_b apart per batch entry
   long long pos_b;
   const double* inv_freq;  // [rot / 2]
-  int B, L, d, rot, axes;
+  int B, L, d, rot;
   int end[4];            // pairs [end[a - 1], end[a]) turn by axis a
   float factor;
   bool half, inverse, bf16;
@@ -178,7 +178,7 @@ cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);
 struct RopeTableArgs {
   const int* pos;  // [axes, L]
   const double* inv_freq;
-  int L, rot, axes;
+  int L, rot;
   int end[4];
   float factor;
   float* cos;  // [L, rot / 2]
