@@ -726,14 +726,17 @@ cudaError_t launch_fwd_k(const NormArgs& a, Shape s, int num_sms, cudaStream_t s
 }
 template <typename T, int V, bool FULL>
 cudaError_t launch_fwd(const NormArgs& a, const Shape& s, int num_sms, cudaStream_t stream) {
-  if constexpr (V > 1) {
+  if constexpr (V == 1) {
+    return s.elems == 8 ? launch_fwd_k<T, V, 8, false, FULL, 1024>(a, s, num_sms, stream)
+                        : launch_fwd_k<T, V, 16, false, FULL, 1024>(a, s, num_sms, stream);
+  } else {
     // two rows in the ring; fp32 rows of more than 7680 channels leave it no room and are read directly
-    if (static_cast<size_t>(s.tpr) * s.elems * (12 + 4 * sizeof(T)) <= kSmemMax)
-      return s.elems == 8 ? launch_fwd_k<T, V, 8, true, FULL, 1024>(a, s, num_sms, stream)
-                          : launch_fwd_k<T, V, 16, true, FULL, 1024>(a, s, num_sms, stream);
+    if constexpr (sizeof(T) == 4) {
+      if (static_cast<size_t>(s.tpr) * s.elems * 28 > kSmemMax) return launch_fwd_k<T, V, 16, false, FULL, 1024>(a, s, num_sms, stream);
+    }
+    return s.elems == 8 ? launch_fwd_k<T, V, 8, true, FULL, 1024>(a, s, num_sms, stream)
+                        : launch_fwd_k<T, V, 16, true, FULL, 1024>(a, s, num_sms, stream);
   }
-  return s.elems == 8 ? launch_fwd_k<T, V, 8, false, FULL, 1024>(a, s, num_sms, stream)
-                      : launch_fwd_k<T, V, 16, false, FULL, 1024>(a, s, num_sms, stream);
 }
 
 template <typename T, int V, int E, bool RING, bool FULL, int MAXT, int MINB>
@@ -747,29 +750,37 @@ cudaError_t launch_bwd_k(const NormBwdArgs& a, const Shape& s, cudaStream_t stre
 }
 template <typename T, int V, int E, bool RING, bool FULL>
 cudaError_t launch_bwd_t(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
-  if constexpr (E == 8) {
-    if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 3>(a, s, stream);
-    if constexpr (V == 1) return launch_bwd_k<T, V, E, RING, FULL, 768, 1>(a, s, stream);
-    else return cudaErrorInvalidValue;  // bwd_elems gives 8 of these to 256 threads at most
-  } else if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 2>(a, s, stream);
-  else return launch_bwd_k<T, V, E, RING, FULL, 512, 1>(a, s, stream);
+  // 8 channels a thread in more than 256 threads, and 16 without the ring in fewer, do not come up (bwd_elems)
+  if constexpr (E == 16) {
+    if constexpr (RING) {
+      if (s.threads <= 256) return launch_bwd_k<T, V, E, RING, FULL, 256, 2>(a, s, stream);
+    }
+    return launch_bwd_k<T, V, E, RING, FULL, 512, 1>(a, s, stream);
+  } else {
+    if constexpr (V == 1) {
+      if (s.threads > 256) return launch_bwd_k<T, V, E, RING, FULL, 768, 1>(a, s, stream);
+    }
+    return launch_bwd_k<T, V, E, RING, FULL, 256, 3>(a, s, stream);
+  }
 }
 template <typename T, int V, bool FULL>
 cudaError_t launch_bwd(const NormBwdArgs& a, const Shape& s, cudaStream_t stream) {
-  if constexpr (V > 1) {
-    // two rows in the ring where they fit; fp32 rows of more than 5376 channels are read directly
-    if (row_bytes(s, 8 + 8 * static_cast<int>(sizeof(T))) <= kSmemMax)
-      return s.elems == 8 ? launch_bwd_t<T, V, 8, true, FULL>(a, s, stream)
-                          : launch_bwd_t<T, V, 16, true, FULL>(a, s, stream);
+  if constexpr (V == 1) {
+    return s.elems == 8 ? launch_bwd_t<T, V, 8, false, FULL>(a, s, stream) : launch_bwd_t<T, V, 16, false, FULL>(a, s, stream);
+  } else {
+    // two rows in the ring; fp32 rows of more than 5120 channels leave it no room and are read directly
+    if constexpr (sizeof(T) == 4) {
+      if (row_bytes(s, 40) > kSmemMax) return launch_bwd_t<T, V, 16, false, FULL>(a, s, stream);
+    }
+    return s.elems == 8 ? launch_bwd_t<T, V, 8, true, FULL>(a, s, stream) : launch_bwd_t<T, V, 16, true, FULL>(a, s, stream);
   }
-  return s.elems == 8 ? launch_bwd_t<T, V, 8, false, FULL>(a, s, stream)
-                      : launch_bwd_t<T, V, 16, false, FULL>(a, s, stream);
 }
 
 }  // namespace
 
 int norm_bwd_chunks(int B, int T, int C, bool vec) {
-  // one to three blocks per SM, as many as fit
+  // one to three blocks per SM, by their threads and registers; of fp32 rows the ring leaves room for fewer, and the
+  // blocks take turns
   const Shape s = shape_of(C, bwd_elems(C, vec));
   const int most = (T + s.rpb - 1) / s.rpb;
   const int blocks = s.threads > 256 ? kNormBwdBlocks / 4 : s.elems == 16 ? kNormBwdBlocks / 2 : kNormBwdBlocks * 3 / 4;
