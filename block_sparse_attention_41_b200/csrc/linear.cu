@@ -14,11 +14,12 @@
 // activation, residual, rounding, and a TMA store per warp out of swizzled shared memory) runs
 // under the products of the next. Large products run on pairs of SMs: a 256 x 256 (or 256 x 128)
 // tile, of which each CTA loads its 128 rows of A and its half of B's rows, and one thread issues the
-// MMAs for both. That halves what shared memory takes in per product for B; a tile of 128 x 256 on one
-// SM is held back there (1.22 PFLOP/s at 33272 x 4096 x 16384, against 1.51 in short bursts and 1.32 under the
-// power cap, gelu included). Few tiles go to single SMs, 128 x 128 or
-// 128 x 64 each, to fill more of them; with a long reduction and a workspace, the tiles past the last whole turn
-// of the SMs go in pieces of the reduction, which a second kernel adds (200 x 4096 -> 4096: 25 us whole, 16 us).
+// MMAs for both. That halves what shared memory takes in per product for B (33272 x 4096 -> 16384 in bursts of
+// five calls: 2.99 to 3.04 ms, 1.47 to 1.49 PFLOP/s, and 3.07 to 3.09 with bias and gelu; 3.47 and 3.53 in calls on
+// end, under the power cap; tiles of 128 x 256 on single SMs, bursts: 3.07 and 3.09). Few tiles go to single SMs,
+// 128 x 128 or 128 x 64 each, to fill more of them; with a long reduction and a workspace, the tiles past the last
+// whole turn of the SMs go in pieces of the reduction, which a second kernel adds (200 x 4096 -> 4096, weights from
+// DRAM: 33 us whole, 19 us).
 //
 // With up to kFewRows rows the layer is bound by reading w once. There the product is taken
 // transposed: 128 rows of w are the M side of the MMA and the tokens its N side, so the ring holds
@@ -51,7 +52,7 @@ constexpr int kPieceSlices = 16;
 constexpr double kPieceCycles = 9000.0;
 // Output rows walked together, column by column: at least 2048, so that a wave of tiles is about square
 // and its tiles share operands as they stream by; with a short reduction as many as keep their part
-// of A in L2 while B passes (at K = 4096, 4096 rows instead of 2048: 2907 against 2968 us).
+// of A in L2 while B passes (at K = 4096, 4096 rows instead of 2048: 3085 against 3140 us, gelu included).
 constexpr int kGroupRows = 2048;
 constexpr double kGroupBytes = 33554432.0;
 
@@ -921,7 +922,7 @@ __global__ void __launch_bounds__(kFewThreads)
 // ---- gradient of the activation and of the bias --------------------------------------------------------
 // dz = dy act'(z) in bf16 (the operand of the two products that follow; the rounding is theirs), and
 // per block of rows the fp32 column sums of the unrounded dz, added by a second kernel in a fixed
-// order. HBM-bound (8192 x 4096 with gelu: 40 us, 5 TB/s): 32 threads side by side cover 256 columns with 16-byte vectors, 8 rows at a time.
+// order. HBM-bound (8192 x 4096 with gelu: 41 us, 4.9 TB/s): 32 threads side by side cover 256 columns with 16-byte vectors, 8 rows at a time.
 constexpr int kDzCols = 256, kDzRows = 8;
 
 __device__ __forceinline__ void widen_bf16(const uint4& v, f2 (&x)[4]) {
@@ -1050,8 +1051,8 @@ cudaError_t launch_few_t(const FewArgs& a, const FewParams& p, cudaStream_t stre
 GemmTile linear_tile(int Mo, int No, int Ko, bool splittable, int num_sms) {
   // SM cycles until the last one is done, from measured products: a slice (64 deep) takes about as long on
   // the smaller tiles, which wait for their operands, as the 512 MMA cycles of the largest; the last
-  // epilogue is not overlapped. (8191 x 768 -> 768 takes 15.2, 18.9, 18.1 and 28.7 us in this order,
-  // 1000 x 768 -> 768 10.5, 10.2, 8.6 and 8.0 us.)
+  // epilogue is not overlapped. (8191 x 768 -> 768 takes 15.5, 18.3, 17.1 and 27.6 us in this order,
+  // 1000 x 768 -> 768 9.5, 8.6, 7.2 and 7.1 us.)
   const struct { int ctas, n; double slice, last; } options[] = {
       {2, 256, 600.0, 6500.0}, {2, 128, 510.0, 6000.0}, {1, 128, 545.0, 4000.0}, {1, 64, 487.0, 3200.0}};
   const int nk = (Ko + BK - 1) / BK;
@@ -1117,7 +1118,7 @@ cudaError_t launch_linear_few(const FewArgs& a, cudaStream_t stream) {
   p.wait_limit_ns = a.wait_limit_ns;
   p.ws = a.ws;
   // the reduction over 1, 2, 4 or 8 CTAs: as many as are resident at once, each with two slices at least
-  // (2 x 5120 -> 30720: 49.7 us over 2, 52.2 over 4; 16 x 4096 -> 4096: 17.3, 12.2 and 11.0 over 2, 4, 8)
+  // (2 x 5120 -> 30720: 50.9 us over 1, 49.9 over 2, 51.9 over 4; 16 x 4096 -> 4096: 25.4, 16.5, 12.0 and 11.1 over 1, 2, 4, 8)
   const int resident = a.num_sms * (a.M <= 16 ? 4 : a.M <= 64 ? 3 : 2);
   const int tiles = (a.N + BM - 1) / BM;
   p.split = 1;

@@ -306,7 +306,7 @@ __device__ __forceinline__ void normalise_back(const L& l, RowGroup& g, f2 (&w)[
 // A block's groups of tpr threads take rows of one batch entry, so they share the vectors' products in
 // shared memory: A = gate post_gain, S = gain (1 + scale), H = shift. (In registers they left room
 // for half as many threads and spilled: 874 us at 75600 x 5120 bf16; read per row from L1, 793 us; this
-// form 479 us, 6.5 TB/s.)
+// form 479 to 517 us on different GPUs, 6.0 to 6.5 TB/s.)
 // RING: the next row is on its way while one is reduced; else direct loads.
 template <typename T, int V, int E, bool RING, bool FULL, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid_constant__ NormArgs p, int tpr, int chunks) {
@@ -423,7 +423,9 @@ __global__ void __launch_bounds__(MAXT, 1) sol_residual_norm_kernel(const __grid
 // go to the workspace once per block, and a second kernel adds the blocks in a fixed order: no
 // atomics, the same bits every time. With three sums, n, ny and w in registers the vectors' products
 // have no room there; they lie in the thread's slots of shared memory. 2 x 33272 x 4096 bf16 with both norms:
-// 659 us, 5.0 TB/s; with 128 registers, 16 warps per SM have to cover four reductions in a row.
+// 659 to 694 us on different GPUs, 4.7 to 5.0 TB/s; with 128 registers, 16 warps per SM have to cover a row's four
+// reductions, one behind the other. (mean(w n) = r mean(w x') does not have to wait for r: its sum could share the
+// exchange of the squares, which is not done here.)
 template <typename T, int V, int E, bool RING, bool FULL, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) sol_residual_norm_bwd_kernel(const __grid_constant__ NormBwdArgs p, int tpr) {
   using L = Lane<T, V, E, FULL>;
@@ -686,9 +688,9 @@ Shape shape_of(int C, int elems) {
   s.threads = s.tpr * s.rpb;
   return s;
 }
-// 16 channels halve the shuffles per value (gradient of 20000 x 5120 bf16: 357 us in ten warps per SM, 434
+// 16 channels halve the shuffles per value (gradient of 20000 x 5120 bf16: 318 us in ten warps per SM, 321
 // in twenty with 8); 8 pad short rows less, and leave the gradient's single values room for an
-// address and a test each (20000 x 5119: 900 us, 1500 with 16 that spill).
+// address and a test each (20000 x 5119: 854 us, 1465 with 16 that spill).
 int fwd_elems(int C) {
   const Shape a = shape_of(C, 16), b = shape_of(C, 8);
   return C > 2048 || 16 * a.tpr <= 8 * b.tpr ? 16 : 8;

@@ -9,7 +9,10 @@
 // pair's turn per position, modulo one, becomes a 64-bit fraction, and the angle is position times
 // fraction in integers, where whole turns fall off by themselves; its top 32 bits are the angle to
 // 2^-32 of a turn. Cosine and sine of what is left of it in the nearest quarter turn come from their
-// Taylor series, good to about 1e-7 at every position. The 64-bit float work is one product per pair.
+// Taylor series in fp32. What that costs, in units of u = 2^-24 with a factor of 1: 0.1 u for the angle cut to 2^-32
+// of a turn (6 u more at the far end of 32-bit positions, for the rounding of the frequency over 2 pi in 64 bits), 1.7 u
+// for its value in radians (converted, times a rounded constant, rounded: 3 u of at most pi / 4, times a slope of 0.71),
+// 1.4 u for the polynomial and the multiplication by the factor: at most 4 u up to positions of 10^7. The 64-bit float work is one product per pair.
 //
 // HBM-bound: every element is read and written once. A thread owns one vector of columns of one token
 // (one of each half in the half layout), of 16 bytes where lengths, strides and addresses allow. It forms
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kTableThreads) sol_rope_tables_kernel(const __
 
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   // the widest access that divides every length, stride and address (half layout, 40000 tokens of 32 heads of
-  // 128: 281 us with 94 channels turned, pair by pair, 133 with 92, two pairs at a time, 114 with 88, four)
+  // 128: 278 us with 94 channels turned, pair by pair, 139 with 92, two pairs at a time, 114 with 88, four)
   if (a.bf16) {
     switch (a.width) {
       case 8: return launch_t<__nv_bfloat16, 8>(a, num_sms, stream);

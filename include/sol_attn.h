@@ -411,7 +411,9 @@ sol_status sol_attn_rope_inv_freq(int rot, double base, int axes, const int* sec
                                   float* attn_factor);
 
 /* Cosine and sine tables, the rope_cos / rope_sin of sol_attn_qknorm_rope_pool (rot = d there):
- * attn_factor * cos and sin of pos[axis(i)][t] * inv_freq[i], angles formed in 64 bits.
+ * attn_factor * cos and sin of pos[axis(i)][t] * inv_freq[i]. An angle is a position times a 64-bit fraction of a turn, in
+ * integers, of which the top 32 bits (1.5e-9 radians) go on; cosine and sine are fp32, off by at most 4 * 2^-24 of the
+ * factor up to positions of 10^7, 10 * 2^-24 up to 2^31 (frequencies up to 1).
  *   pos          device, int32 [axes, L]
  *   sections     HOST, int [axes], or NULL for one axis
  *   inv_freq     device, double [rot / 2]
